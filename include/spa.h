@@ -310,6 +310,142 @@ SPA_API int spa_attention_decode(const void *q, const void *P, const void *kc, c
                                  int d_v, int cap, int dtype, void *stream);
 
 /*
+ * Serving a batch from the projected key cache.  A decode loop calls, per
+ * step: spa_rope on the new queries and keys, spa_kcache_append_ragged,
+ * spa_attention_decode_shared, and spa_kcache_evict when the cache is to stay
+ * within a budget.  The caches are those of spa_kcache_append with Hk key
+ * heads; H = G * Hk query heads, of which h*G .. h*G+G-1 share key head h and
+ * its projection P [Hk][d][m].  Lengths and positions are device arrays, so a
+ * captured graph replays with the values of the day.  A length outside
+ * [0, cap] counts as the nearer bound, and a row outside the cache is not
+ * written.  lens, pos, count, token, row_pos and src are int32; these, acc and
+ * the multipliers are 4-byte aligned.
+ *
+ * spa_rope -- rotary positions on one or two tensors (queries, and the keys
+ *   that share their positions) in one launch: feature pair i of the row at
+ *   position n turns by the angle n * f_i,
+ *     (a, b) -> scale * (a cos - b sin, a sin + b cos);
+ *   pair i is features (2i, 2i+1) (interleaved != 0) or (i, i + rot/2), and
+ *   features rot .. d-1 are copied.  inverse != 0 turns the other way: with
+ *   the upstream gradient as input that is the gradient.
+ *     q, q_out  [B][H][N][d]; k, k_out [B][Hk][N][d] (Hk = 0: none, NULL), of
+ *               `dtype`, aligned to their elements.  An output may be its
+ *               input (same strides); any other overlap is not allowed.
+ *     strides   NULL: all dense.  Else 12 host values, in elements: batch,
+ *               head and row of q, k, q_out, k_out (features adjacent).  The
+ *               rows of an output must not overlap (SPA_ERR_SHAPE); inputs
+ *               may repeat rows (stride 0).
+ *     pos       [B][N] device, or NULL: row n is at pos0 + n.
+ *     table     [rot/2] device, from spa_rope_table.
+ *   1 <= d <= 1024, rot even, 2 <= rot <= d.  Angles are formed without
+ *   rounding modulo one turn at every position, arithmetic is fp32.
+ * spa_rope_table (host) -- table[i] = round(inv_freq[i] / 2pi * 2^64) mod 2^64
+ *   for the rot/2 frequencies f_i (host arrays; finite, else SPA_ERR_SHAPE):
+ *   the advance per position in units of 2^-64 turns.
+ * spa_rope_frequencies (host) -- inv_freq[i] = base^(-2i/rot), stretched for
+ *   contexts `factor` times as long as the trained length:
+ *     SPA_ROPE_PLAIN   as it is
+ *     SPA_ROPE_LINEAR  f_i / factor (interpolated positions)
+ *     SPA_ROPE_BASE    base * factor^(rot/(rot-2)) in the place of base
+ *                      (rot >= 4; the slowest pair slows down by `factor`)
+ *     SPA_ROPE_RAMP    by the turns r_i = trained * f_i / 2pi that pair i
+ *                      makes over the trained length: f_i where r_i >= fast,
+ *                      f_i / factor where r_i <= slow, and the blend that is
+ *                      linear in r_i between (0 <= slow < fast)
+ */
+typedef enum {
+  SPA_ROPE_PLAIN = 0,
+  SPA_ROPE_LINEAR = 1,
+  SPA_ROPE_BASE = 2,
+  SPA_ROPE_RAMP = 3
+} spa_rope_scaling;
+SPA_API int spa_rope_frequencies(double *inv_freq, int rot, double base, int scaling,
+                                 double factor, double trained, double slow, double fast);
+SPA_API int spa_rope_table(const double *inv_freq, int rot, unsigned long long *table);
+SPA_API int spa_rope(const void *q, const void *k, void *q_out, void *k_out,
+                     const long long *strides, const int *pos, int pos0,
+                     const unsigned long long *table, int B, int H, int Hk, int N, int d, int rot,
+                     int interleaved, int inverse, float scale, int dtype, void *stream);
+
+/*
+ * spa_kcache_append_ragged -- spa_kcache_append at a row of its own for every
+ *   sequence, with the value rows: of k [B][H][T][d] and v [B][H][T][d_v]
+ *   (bf16; H key heads here) the first count[b] (NULL: T) rows go to cache
+ *   rows pos[b] .. of kc, kc_mul and vc [B][H][cap][d_v].  Rows are as
+ *   spa_kcache_append writes them, up to the order of the fp32 sums, with the
+ *   multiplier of the exact row maximum.  For the eviction, the new rows of
+ *   acc [B][H][cap] are set to 0 and those of row_pos [B][H][cap] to token[b]
+ *   + t (NULL: pos[b] + t); acc and row_pos may be NULL.  No two sequences
+ *   share rows, so the calls of a graph replay bit for bit.
+ */
+SPA_API int spa_kcache_append_ragged(const void *k, const void *v, const void *P, void *kc,
+                                     float *kc_mul, void *vc, const int *pos, const int *count,
+                                     float *acc, int *row_pos, const int *token, int B, int H,
+                                     int T, int d, int m, int d_v, int cap, int dtype,
+                                     void *stream);
+
+/*
+ * spa_attention_decode_shared -- one query per (sequence, head), q [B][H][d]
+ *   (bf16), against rows 0 .. plen-1 of a prefix that all sequences share
+ *   (pkc [Hk][pcap][m], pkc_mul, pv [Hk][pcap][d_v]: a cache of batch 1) and
+ *   rows 0 .. lens[b]-1 of the sequence's own cache (kc, kc_mul, v as above,
+ *   cap rows), in one softmax:
+ *     out[b][h][:] = softmax(<q P, K~_j> / sqrt(m)) V        bf16 [B][H][d_v]
+ *   The prefix is read once for the whole batch.  A query without any key
+ *   (plen = 0 and lens[b] = 0) gets 0.  plen = 0 needs no prefix (NULL), cap =
+ *   0 no caches of the sequences (NULL, lens too).  Rows at and behind a
+ *   length may hold anything, infinities and NaN included.
+ *   Weights: with acc and acc_out [B][Hk][cap] (both or neither; they may be
+ *   the same array) the weight that this step's queries give to each own row,
+ *   summed over the G heads of a group, is added: acc_out = acc + sum_g p_gj
+ *   for rows below the length; the others are left as they are.
+ *   workspace: device, 256-byte aligned, at least
+ *   spa_attention_decode_shared_workspace_size bytes, overwritten, for this
+ *   call alone until it has run; NULL: from the library's pool.
+ *   Scores, softmax statistics and sums are fp32.  SPA_BF16 only; 1 <= d <=
+ *   256, m in {16, 32, 64, 128}, d_v in {64, 128}, H a multiple of Hk,
+ *   B*H <= 65535.
+ */
+SPA_API int spa_attention_decode_shared_workspace_size(int B, int H, int Hk, int plen, int d,
+                                                       int m, int d_v, int cap, int weights,
+                                                       size_t *bytes);
+SPA_API int spa_attention_decode_shared(const void *q, const void *P, const void *kc,
+                                        const float *kc_mul, const void *v, const int *lens,
+                                        const void *pkc, const float *pkc_mul, const void *pv,
+                                        void *out, const float *acc, float *acc_out, int B, int H,
+                                        int Hk, int plen, int pcap, int d, int m, int d_v, int cap,
+                                        int dtype, void *workspace, size_t workspace_bytes,
+                                        void *stream);
+
+/*
+ * spa_kcache_evict -- brings every sequence's cache down to `budget` rows, in
+ *   place.  Of the lens[b] rows of a (sequence, key head) there stay, up to
+ *   budget: first the protected ones, whose token position row_pos is below
+ *   `sink` or among the newest `recent` positions (above the largest one less
+ *   `recent`); then those of largest acc, ties to the lower row, NaN last.
+ *   Rows that stay and lie below the new length min(lens[b], budget) keep
+ *   their place; the others, in ascending order, take the places of the
+ *   evicted ones in ascending order: attention does not depend on the order
+ *   of rows, and a step that drops one row moves one row.
+ *     kc, kc_mul, v             the cache, rows moved in place; rows at and
+ *                               behind the new length are left as they are
+ *     acc, row_pos              [B][H][cap], read; acc_out, row_pos_out: their
+ *                               values in the new order (rows below the new
+ *                               length; each may be its input)
+ *     lens_out                  [B] the new lengths (may be lens)
+ *     src                       [B][H][budget] the row that each row was
+ *                               before, -1 behind the new length
+ *   1 <= budget <= cap, sink, recent >= 0, sink + recent <= budget, else
+ *   SPA_ERR_SHAPE; m, d_v as above, B*H <= 65535.  workspace as above.
+ */
+SPA_API int spa_kcache_evict_workspace_size(int B, int H, int cap, int budget, size_t *bytes);
+SPA_API int spa_kcache_evict(void *kc, float *kc_mul, void *v, const float *acc,
+                             const int *row_pos, const int *lens, float *acc_out,
+                             int *row_pos_out, int *lens_out, int *src, int B, int H, int m,
+                             int d_v, int cap, int budget, int sink, int recent, void *workspace,
+                             size_t workspace_bytes, void *stream);
+
+/*
  * Sparse Feature Attention ("Scaling Attention via Feature Sparsity" notes,
  * Sec. 1 and Sec. 3): every query and key row keeps its k features of largest
  * magnitude and zeroes the rest, and attention runs on the sparsified rows,

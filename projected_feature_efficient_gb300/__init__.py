@@ -21,6 +21,10 @@ __all__ = [
     "spa_attention_fwd_lse", "spa_attention_bwd_lse", "spa_attention_bwd_workspace_size",
     "spa_attention_bwd_prepare", "spa_attention_bwd_apply", "spa_attention_bwd_finish",
     "host_pool_trim",
+    "SPA_ROPE_PLAIN", "SPA_ROPE_LINEAR", "SPA_ROPE_BASE", "SPA_ROPE_RAMP", "rope_frequencies",
+    "rope_table", "spa_rope", "spa_kcache_append_ragged",
+    "spa_attention_decode_shared_workspace_size", "spa_attention_decode_shared",
+    "spa_kcache_evict_workspace_size", "spa_kcache_evict",
 ]
 
 

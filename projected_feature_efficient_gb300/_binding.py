@@ -76,6 +76,24 @@ lib.spa_kcache_append.argtypes = [_vp] * 4 + [_i] * 8 + [_vp]
 lib.spa_kcache_append.restype = _i
 lib.spa_attention_decode.argtypes = [_vp] * 6 + [_i] * 8 + [_vp]
 lib.spa_attention_decode.restype = _i
+_d, _ll, _pd = ctypes.c_double, ctypes.c_longlong, ctypes.POINTER(ctypes.c_double)
+lib.spa_rope_frequencies.argtypes = [_pd, _i, _d, _i, _d, _d, _d, _d]
+lib.spa_rope_frequencies.restype = _i
+lib.spa_rope_table.argtypes = [_pd, _i, ctypes.POINTER(ctypes.c_ulonglong)]
+lib.spa_rope_table.restype = _i
+lib.spa_rope.argtypes = ([_vp] * 4 + [ctypes.POINTER(_ll), _vp, _i, _vp] + [_i] * 8 +
+                         [ctypes.c_float, _i, _vp])
+lib.spa_rope.restype = _i
+lib.spa_kcache_append_ragged.argtypes = [_vp] * 11 + [_i] * 8 + [_vp]
+lib.spa_kcache_append_ragged.restype = _i
+lib.spa_attention_decode_shared_workspace_size.argtypes = [_i] * 9 + [ctypes.POINTER(_sz)]
+lib.spa_attention_decode_shared_workspace_size.restype = _i
+lib.spa_attention_decode_shared.argtypes = [_vp] * 12 + [_i] * 10 + [_vp, _sz, _vp]
+lib.spa_attention_decode_shared.restype = _i
+lib.spa_kcache_evict_workspace_size.argtypes = [_i] * 4 + [ctypes.POINTER(_sz)]
+lib.spa_kcache_evict_workspace_size.restype = _i
+lib.spa_kcache_evict.argtypes = [_vp] * 10 + [_i] * 8 + [_vp, _sz, _vp]
+lib.spa_kcache_evict.restype = _i
 
 
 class SpaError(RuntimeError):
@@ -354,6 +372,260 @@ def spa_attention_decode(q, P, kc, kc_mul, v, L, out=None, stream=None):
                                     B, H, L, d, m, dv, cap, _dtype_code(q), _stream_ptr(stream)),
            "spa_attention_decode")
     return out
+
+
+SPA_ROPE_PLAIN, SPA_ROPE_LINEAR, SPA_ROPE_BASE, SPA_ROPE_RAMP = 0, 1, 2, 3
+
+
+class _On:
+    """The device and stream of a call: the arguments' device is made current
+    for its duration, and `stream` (default: the device's current one) is the
+    stream of its launches and of the tensors it allocates."""
+
+    __slots__ = ("index", "raw", "_guards")
+
+    def __init__(self, device, stream):
+        import torch
+        self.index = device.index
+        self._guards = ()
+        if stream is not None:
+            if stream.device_index != device.index:
+                raise ValueError("the stream belongs to another device than the tensors")
+            self._guards = (torch.cuda.stream(stream),)
+            self.raw = stream.cuda_stream
+        else:
+            if torch.cuda.current_device() != device.index:
+                self._guards = (torch.cuda.device(device.index),)
+            self.raw = torch._C._cuda_getCurrentRawStream(device.index)
+
+    def __enter__(self):
+        for g in self._guards:
+            g.__enter__()
+        return self
+
+    def __exit__(self, *exc):
+        for g in reversed(self._guards):
+            g.__exit__(*exc)
+
+
+def _device_of(t):
+    if not t.is_cuda:
+        raise ValueError("the tensors of this call are CUDA tensors")
+    return t.device
+
+
+def _arg(name, t, shape, dtype, device):
+    """A dense tensor of this shape, type and device; its address."""
+    if t.shape != shape:
+        raise ValueError(f"{name} must have the shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _workspace(t, device):
+    """Address and size of a caller's workspace (None: the library takes its own)."""
+    if t is None:
+        return None, 0
+    if t.device != device:
+        raise ValueError(f"workspace must be on {device}, got {t.device}")
+    if not t.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return t.data_ptr(), t.nbytes
+
+
+def rope_frequencies(rot, base=10000.0, scaling=SPA_ROPE_PLAIN, factor=1.0, trained=0.0, slow=1.0,
+                     fast=32.0):
+    """The rot/2 frequencies base^(-2i/rot) as a float64 CPU tensor, stretched
+    for long contexts (scaling: SPA_ROPE_LINEAR, _BASE or _RAMP; see spa.h)."""
+    import torch
+    f = torch.empty(max(int(rot), 0) // 2, dtype=torch.float64)
+    _check(lib.spa_rope_frequencies(ctypes.cast(f.data_ptr(), _pd), int(rot), base, int(scaling),
+                                    factor, trained, slow, fast), "spa_rope_frequencies")
+    return f
+
+
+def rope_table(inv_freq, device="cuda"):
+    """The table that spa_rope takes, from the rot/2 frequencies (radians per
+    position): an int64 tensor on `device` of advances in units of 2^-64 turns."""
+    import torch
+    f = torch.as_tensor(inv_freq, dtype=torch.float64, device="cpu").contiguous()
+    if f.dim() != 1:
+        raise ValueError("inv_freq must have one dimension")
+    t = torch.empty(f.shape, dtype=torch.int64)
+    _check(lib.spa_rope_table(ctypes.cast(f.data_ptr(), _pd), 2 * f.numel(),
+                              ctypes.cast(t.data_ptr(), ctypes.POINTER(ctypes.c_ulonglong))),
+           "spa_rope_table")
+    return t.to(device)
+
+
+_Strides = _ll * 12
+
+
+def spa_rope(q, table, pos=None, *, k=None, rot=None, interleaved=False, inverse=False, scale=1.0,
+             pos0=0, out=None, k_out=None, stream=None):
+    """Rotary positions of q [B,H,N,d] and, in the same launch, k [B,Hk,N,d]
+    (bf16 or fp32, any strides with adjacent features); returns the rotated
+    tensor, or both.  pos is [B,N] int32 (default: pos0 + n).  inverse=True maps
+    the outputs' gradients to the inputs'."""
+    import torch
+    device = _device_of(q)
+    B, H, N, d = q.shape
+    rot = 2 * table.numel() if rot is None else int(rot)
+    ptable = _arg("table", table, (rot // 2,), torch.int64, device)
+    ppos = None if pos is None else _arg("pos", pos, (B, N), torch.int32, device)
+    code = _dtype_code(q)
+    Hk = 0
+    if k is not None:
+        Hk = k.shape[1]
+        if k.shape != (B, Hk, N, d):
+            raise ValueError("k must be [B,Hk,N,d] with q's B, N and d")
+        if k.dtype != q.dtype:
+            raise TypeError("q and k must share one dtype")
+        if k.device != device:
+            raise ValueError(f"k must be on {device}, got {k.device}")
+    elif k_out is not None:
+        raise ValueError("k_out without k")
+    with _On(device, stream) as on:
+        if out is None:
+            out = torch.empty((B, H, N, d), dtype=q.dtype, device=device)
+        if k is not None and k_out is None:
+            k_out = torch.empty((B, Hk, N, d), dtype=q.dtype, device=device)
+        for x, y in ((q, out), (k, k_out)):
+            if x is None:
+                continue
+            if y.shape != x.shape or y.dtype != x.dtype or y.device != device:
+                raise ValueError("an output must have its input's shape, dtype and device")
+            if (x.stride(3) != 1 or y.stride(3) != 1) and d > 1:
+                raise ValueError("the features of a row must be adjacent")
+        a, c = q.stride(), out.stride()
+        b, e = (k.stride(), k_out.stride()) if k is not None else ((0, 0, 0), (0, 0, 0))
+        strides = _Strides(a[0], a[1], a[2], b[0], b[1], b[2], c[0], c[1], c[2], e[0], e[1], e[2])
+        _check(lib.spa_rope(q.data_ptr(), k.data_ptr() if Hk else None, out.data_ptr(),
+                            k_out.data_ptr() if Hk else None, strides, ppos, pos0, ptable, B, H, Hk,
+                            N, d, rot, bool(interleaved), bool(inverse), scale, code, on.raw),
+               "spa_rope")
+    return out if k is None else (out, k_out)
+
+
+def spa_kcache_append_ragged(k, v, P, kc, kc_mul, vc, pos, count=None, acc=None, row_pos=None,
+                             token=None, stream=None):
+    """The first count[b] (default: T) rows of k [B,H,T,d] (projected with P
+    [H,d,m]) and v [B,H,T,dv], bf16, into cache rows pos[b].. of every sequence;
+    acc and row_pos (for spa_kcache_evict) start at 0 and token[b] + t."""
+    import torch
+    device = _device_of(k)
+    B, H, T, d = k.shape
+    m, cap, dv = P.shape[-1], kc.shape[2], v.shape[-1]
+    bf16, i32, f32 = torch.bfloat16, torch.int32, torch.float32
+    row = (B, H, cap)
+    args = (_arg("k", k, (B, H, T, d), bf16, device), _arg("v", v, (B, H, T, dv), bf16, device),
+            _arg("P", P, (H, d, m), bf16, device),
+            _arg("kc", kc, (B, H, cap, m), torch.int16, device),
+            _arg("kc_mul", kc_mul, row, f32, device),
+            _arg("vc", vc, (B, H, cap, dv), bf16, device),
+            _arg("pos", pos, (B,), i32, device),
+            None if count is None else _arg("count", count, (B,), i32, device),
+            None if acc is None else _arg("acc", acc, row, f32, device),
+            None if row_pos is None else _arg("row_pos", row_pos, row, i32, device),
+            None if token is None else _arg("token", token, (B,), i32, device))
+    with _On(device, stream) as on:
+        _check(lib.spa_kcache_append_ragged(*args, B, H, T, d, m, dv, cap, SPA_BF16, on.raw),
+               "spa_kcache_append_ragged")
+
+
+def spa_attention_decode_shared_workspace_size(B, H, Hk, plen, d, m, dv, cap, weights=False) -> int:
+    n = _sz(0)
+    _check(lib.spa_attention_decode_shared_workspace_size(B, H, Hk, plen, d, m, dv, cap,
+                                                          bool(weights), ctypes.byref(n)),
+           "spa_attention_decode_shared_workspace_size")
+    return int(n.value)
+
+
+def spa_attention_decode_shared(q, P, kc, kc_mul, v, lens, *, prefix=None, plen=None, acc=None,
+                                acc_out=None, out=None, workspace=None, stream=None):
+    """One query per (sequence, head), q [B,H,d] bf16, against a prefix shared by
+    the batch, prefix = (kc [Hk,pcap,m], kc_mul [Hk,pcap], v [Hk,pcap,dv]) of
+    which plen rows (default: all) count, and rows 0..lens[b]-1 of the own
+    caches kc [B,Hk,cap,m], kc_mul, v; returns bf16 [B,H,dv].  With acc
+    [B,Hk,cap] the step's attention weights are added to it (into acc_out,
+    default: acc itself)."""
+    import torch
+    device = _device_of(q)
+    B, H, d = q.shape
+    Hk, m = P.shape[0], P.shape[-1]
+    cap, dv = v.shape[2], v.shape[3]
+    bf16, f32, i16 = torch.bfloat16, torch.float32, torch.int16
+    own = (_arg("q", q, (B, H, d), bf16, device), _arg("P", P, (Hk, d, m), bf16, device),
+           _arg("kc", kc, (B, Hk, cap, m), i16, device),
+           _arg("kc_mul", kc_mul, (B, Hk, cap), f32, device),
+           _arg("v", v, (B, Hk, cap, dv), bf16, device),
+           _arg("lens", lens, (B,), torch.int32, device))
+    shared, pcap = (None, None, None), 0
+    if prefix is not None:
+        pkc, pmul, pv = prefix
+        pcap = pkc.shape[1]
+        shared = (_arg("prefix kc", pkc, (Hk, pcap, m), i16, device),
+                  _arg("prefix kc_mul", pmul, (Hk, pcap), f32, device),
+                  _arg("prefix v", pv, (Hk, pcap, dv), bf16, device))
+    plen = pcap if plen is None else int(plen)
+    if acc_out is None:
+        acc_out = acc
+    weights = (None if acc is None else _arg("acc", acc, (B, Hk, cap), f32, device),
+               None if acc_out is None else _arg("acc_out", acc_out, (B, Hk, cap), f32, device))
+    with _On(device, stream) as on:
+        if out is None:
+            out = torch.empty((B, H, dv), dtype=bf16, device=device)
+        pout = _arg("out", out, (B, H, dv), bf16, device)
+        ws, size = _workspace(workspace, device)
+        _check(lib.spa_attention_decode_shared(*own, *shared, pout, *weights, B, H, Hk, plen, pcap,
+                                               d, m, dv, cap, SPA_BF16, ws, size, on.raw),
+               "spa_attention_decode_shared")
+    return out
+
+
+def spa_kcache_evict_workspace_size(B, H, cap, budget) -> int:
+    n = _sz(0)
+    _check(lib.spa_kcache_evict_workspace_size(B, H, cap, budget, ctypes.byref(n)),
+           "spa_kcache_evict_workspace_size")
+    return int(n.value)
+
+
+def spa_kcache_evict(kc, kc_mul, v, acc, row_pos, lens, budget, sink=0, recent=0, acc_out=None,
+                     row_pos_out=None, lens_out=None, src=None, workspace=None, stream=None):
+    """Brings the cache (kc [B,H,cap,m], kc_mul, v) down to `budget` rows per
+    (sequence, head), in place: the first `sink` positions, the newest `recent`
+    ones and the rows of largest acc stay.  acc, row_pos and lens are updated
+    in place unless *_out tensors are given.  Returns src [B,H,budget] int32:
+    the row that each row was before (-1 behind the new length)."""
+    import torch
+    device = _device_of(kc)
+    B, H, cap, m = kc.shape
+    dv, budget = v.shape[-1], int(budget)
+    f32, i32 = torch.float32, torch.int32
+    row = (B, H, cap)
+    acc_out = acc if acc_out is None else acc_out
+    row_pos_out = row_pos if row_pos_out is None else row_pos_out
+    lens_out = lens if lens_out is None else lens_out
+    args = (_arg("kc", kc, (B, H, cap, m), torch.int16, device),
+            _arg("kc_mul", kc_mul, row, f32, device),
+            _arg("v", v, (B, H, cap, dv), torch.bfloat16, device),
+            _arg("acc", acc, row, f32, device), _arg("row_pos", row_pos, row, i32, device),
+            _arg("lens", lens, (B,), i32, device), _arg("acc_out", acc_out, row, f32, device),
+            _arg("row_pos_out", row_pos_out, row, i32, device),
+            _arg("lens_out", lens_out, (B,), i32, device))
+    with _On(device, stream) as on:
+        if src is None:
+            src = torch.empty((B, H, max(budget, 0)), dtype=i32, device=device)
+        psrc = _arg("src", src, (B, H, max(budget, 0)), i32, device)
+        ws, size = _workspace(workspace, device)
+        _check(lib.spa_kcache_evict(*args, psrc, B, H, m, dv, cap, budget, int(sink), int(recent),
+                                    ws, size, on.raw), "spa_kcache_evict")
+    return src
 
 
 def selftest_wait_timeout(limit_ms: int = 50) -> int:

@@ -1,0 +1,228 @@
+// append.cu -- the new keys and values of a ragged batch into the projected
+// key cache: row pos[b] + t of sequence b receives K~ = k P_h in fp16 with its
+// power-of-two multiplier, and the value row as it is.
+//
+// Per key head the rows of all sequences are one matrix [B*T][d] times P_h, so
+// a decode step (T = 1) fills the 16-row tiles of the tensor cores with the
+// sequences of the batch.  Rows are independent: a row's bits depend on the
+// row alone.
+//
+// The row multiplier 2^e puts the row's largest magnitude in [2^13, 2^14).
+// Where the fp32 maximum is within 2^-17 of a power of two, which side it is
+// on is decided on sums in 64 bits, so that the multiplier is the exact one.
+#include <math.h>
+
+#include "kernels.cuh"
+#include "ptx.cuh"
+
+namespace spa {
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kThreads = 32 * kWarps;
+
+__device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }
+
+// e with top * 2^-e in [2^13, 2^14); 0 for a row without a finite magnitude
+__device__ __forceinline__ int row_exponent(double top) {
+  if (!(top > 0.0) || !isfinite(top)) return 0;
+  int E;
+  frexp(top, &E);
+  return max(-125, min(125, E - 14));
+}
+
+__device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t pair_at(const __nv_bfloat16* x, int k, int d) {
+  const uint32_t lo = k < d ? __bfloat16_as_ushort(x[k]) : 0u;
+  const uint32_t hi = k + 1 < d ? __bfloat16_as_ushort(x[k + 1]) : 0u;
+  return lo | (hi << 16);
+}
+
+// P_h as mma B fragments in shared memory: fragment (step, tile) holds for
+// lane l the pairs of rows k0..k0+3 (see below) of column n(l, tile).
+//   features: the sum over k may run in any order, so lane quarter q of a group
+//   of 32 features takes features 8q .. 8q+7, which it reads with one 16-byte
+//   load: step s of the group uses 8q + 4s + {0,1} and 8q + 4s + {2,3}.
+//   columns: tile j, quarter q, holds columns q*(M/4) + 2j + {0,1} of a row, so
+//   a lane ends up with M/4 adjacent columns of the result.
+template <int M>
+__device__ __forceinline__ void stage_projection(uint2* frag, const __nv_bfloat16* P, int d,
+                                                 int groups, int tid) {
+  uint16_t* f = reinterpret_cast<uint16_t*>(frag);
+  for (int i = tid; i < groups * 32 * M; i += kThreads) {
+    const int k = i / M, n = i % M;
+    const uint16_t w = k < d ? __bfloat16_as_ushort(P[i]) : uint16_t(0);
+    const int g = k >> 5, q = (k >> 3) & 3, r = k & 7;
+    const int step = 2 * g + (r >> 2), pos = r & 3;  // pos 0,1: first register, 2,3: second
+    // column n = qn*(M/4) + 2j + o is fragment column 2*qn + o of tile j
+    const int qn = n / (M / 4), j = (n % (M / 4)) >> 1, o = n & 1;
+    const int lane = (2 * qn + o) * 4 + q;  // B fragment: lane = column * 4 + quarter
+    f[((step * (M / 8) + j) * 32 + lane) * 4 + pos] = w;
+  }
+}
+
+template <int M>
+__global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p, int tiles) {
+  extern __shared__ uint2 frag[];
+  const int h = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int q = lane & 3, r0 = lane >> 2;
+  const int groups = (p.d + 31) / 32;
+  const __nv_bfloat16* P = p.P + static_cast<size_t>(h) * p.d * M;
+  stage_projection<M>(frag, P, p.d, groups, tid);
+  __syncthreads();
+  const long long R = static_cast<long long>(p.B) * p.T;
+  const bool wide = p.d % 8 == 0;
+  for (int tile = blockIdx.x * kWarps + warp; tile < tiles; tile += gridDim.x * kWarps) {
+    // this lane's two rows: where they come from and where they go (-1: nowhere)
+    const __nv_bfloat16* x[2];
+    long long dst[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const long long r = static_cast<long long>(tile) * 16 + r0 + 8 * i;
+      x[i] = nullptr;
+      dst[i] = -1;
+      if (r < R) {
+        const int b = static_cast<int>(r / p.T), t = static_cast<int>(r - static_cast<long long>(b) * p.T);
+        const long long at = static_cast<long long>(p.pos[b]) + t;
+        if ((!p.count || t < p.count[b]) && at >= 0 && at < p.cap) {
+          x[i] = p.k + (static_cast<size_t>(b) * p.H + h) * p.T * p.d + static_cast<size_t>(t) * p.d;
+          dst[i] = (static_cast<long long>(b) * p.H + h) * p.cap + at;
+          if (q == 0) {
+            if (p.acc) p.acc[dst[i]] = 0.f;
+            if (p.row_pos) p.row_pos[dst[i]] = (p.token ? p.token[b] : p.pos[b]) + t;
+          }
+        }
+      }
+    }
+    float c[M / 8][4];
+#pragma unroll
+    for (int j = 0; j < M / 8; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) c[j][e] = 0.f;
+    for (int g = 0; g < groups; ++g) {
+      uint32_t w[2][4];
+      const int k = 32 * g + 8 * q;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        if (x[i] && wide && k < p.d) {
+          const uint4 v = __ldg(reinterpret_cast<const uint4*>(x[i] + k));
+          w[i][0] = v.x; w[i][1] = v.y; w[i][2] = v.z; w[i][3] = v.w;
+        } else if (x[i] && !wide) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) w[i][e] = pair_at(x[i], k + 2 * e, p.d);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) w[i][e] = 0u;
+        }
+      }
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        const uint32_t a[4] = {w[0][2 * s], w[1][2 * s], w[0][2 * s + 1], w[1][2 * s + 1]};
+        const uint2* f = frag + ((2 * g + s) * (M / 8)) * 32 + lane;
+#pragma unroll
+        for (int j = 0; j < M / 8; ++j) {
+          const uint2 b = f[j * 32];
+          mma_bf16(c[j], a, b.x, b.y);
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      float top = 0.f;
+#pragma unroll
+      for (int j = 0; j < M / 8; ++j) top = fmaxf(top, fmaxf(fabsf(c[j][2 * i]), fabsf(c[j][2 * i + 1])));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      int e = row_exponent(top);
+      // rows whose maximum is next to a power of two: exact sums decide
+      const uint32_t mant = __float_as_uint(top) & 0x7fffffu;
+      const bool near = dst[i] >= 0 && top > 0.f && isfinite(top) && (mant < 64u || mant > 0x7fffffu - 64u);
+      uint32_t todo = __ballot_sync(0xffffffffu, near && q == 0);
+      while (todo) {
+        const int from = __ffs(todo) - 1;
+        todo &= todo - 1;
+        const __nv_bfloat16* xr = reinterpret_cast<const __nv_bfloat16*>(
+            __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(x[i]), from));
+        double best = 0.0;
+        for (int n = lane; n < M; n += 32) {
+          double s = 0.0;
+          for (int k = 0; k < p.d; ++k)
+            s += static_cast<double>(__bfloat162float(xr[k])) * static_cast<double>(__bfloat162float(P[k * M + n]));
+          best = fmax(best, fabs(s));
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) best = fmax(best, __shfl_xor_sync(0xffffffffu, best, o));
+        if ((lane >> 2) == (from >> 2)) e = row_exponent(best);
+      }
+      if (dst[i] < 0) continue;
+      const float down = pow2i(-e);
+      // this lane's M/4 adjacent columns
+      uint32_t hw[M / 8];
+#pragma unroll
+      for (int j = 0; j < M / 8; ++j) {
+        const __half2 v = __floats2half2_rn(c[j][2 * i] * down, c[j][2 * i + 1] * down);
+        hw[j] = *reinterpret_cast<const uint32_t*>(&v);
+      }
+      uint16_t* o = p.kc + dst[i] * M + q * (M / 4);
+      if constexpr (M == 16) {
+        *reinterpret_cast<uint2*>(o) = make_uint2(hw[0], hw[1]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < M / 8; j += 4)
+          *reinterpret_cast<uint4*>(o + 2 * j) = make_uint4(hw[j], hw[j + 1], hw[j + 2], hw[j + 3]);
+      }
+      if (q == 0) p.kc_mul[dst[i]] = pow2i(e);
+    }
+    // the value rows of the tile, 16 bytes per lane
+    const int pieces = p.dv / 8;
+    for (int i = lane; i < 16 * pieces; i += 32) {
+      const int row = i / pieces, piece = i % pieces;
+      const long long r = static_cast<long long>(tile) * 16 + row;
+      if (r >= R) break;
+      const int b = static_cast<int>(r / p.T), t = static_cast<int>(r - static_cast<long long>(b) * p.T);
+      const long long at = static_cast<long long>(p.pos[b]) + t;
+      if ((p.count && t >= p.count[b]) || at < 0 || at >= p.cap) continue;
+      const size_t from = ((static_cast<size_t>(b) * p.H + h) * p.T + t) * p.dv + piece * 8;
+      const size_t to = ((static_cast<size_t>(b) * p.H + h) * p.cap + at) * p.dv + piece * 8;
+      *reinterpret_cast<uint4*>(p.vc + to) = __ldg(reinterpret_cast<const uint4*>(p.v + from));
+    }
+  }
+}
+
+template <int M>
+cudaError_t launch(const AppendParams& p, cudaStream_t stream) {
+  const long long R = static_cast<long long>(p.B) * p.T;
+  const long long tiles = (R + 15) / 16;
+  if (tiles > 0x7fffffffLL) return cudaErrorInvalidValue;
+  const int smem = (p.d + 31) / 32 * 32 * M * 2;
+  cudaError_t e = cudaFuncSetAttribute(append_kernel<M>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  long long blocks = (tiles + kWarps - 1) / kWarps;
+  const long long most = (152LL * 8 + p.H - 1) / p.H;
+  if (blocks > most) blocks = most;
+  append_kernel<M><<<dim3(static_cast<unsigned>(blocks), p.H), kThreads, smem, stream>>>(
+      p, static_cast<int>(tiles));
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_append_ragged(const AppendParams& p, cudaStream_t stream) {
+  switch (p.m) {
+    case 16: return launch<16>(p, stream);
+    case 32: return launch<32>(p, stream);
+    case 64: return launch<64>(p, stream);
+    case 128: return launch<128>(p, stream);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace spa

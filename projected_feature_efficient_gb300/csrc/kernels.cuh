@@ -180,4 +180,80 @@ struct DecodeParams {
 void decode_split(int BH, int L, int sms, int* nsplit, int* chunk);
 cudaError_t launch_decode(const DecodeParams& p, cudaStream_t stream);
 
+// ---- serving operators around the projected key cache ----
+
+// Rotary positions of up to two tensors that share positions (queries and keys).
+struct RopeParams {
+  const void* x[2];        // inputs, element (b, h, n, c) at b*xs[0] + h*xs[1] + n*xs[2] + c
+  void* y[2];              // outputs, the same with ys
+  long long xs[2][3], ys[2][3];
+  int H[2];                // heads of each tensor (H[1] = 0: one tensor)
+  const int* pos;          // [B][N] positions, or NULL: pos0 + n
+  const unsigned long long* table;  // [rot/2] advance per position in units of 2^-64 turns
+  int B, N, d, rot, pos0;
+  int interleaved, inverse, bf16;
+  float scale;             // multiplies the rotated features
+};
+cudaError_t launch_rope(const RopeParams& p, cudaStream_t stream);
+
+// New keys and values of a ragged batch into the projected key cache.
+struct AppendParams {
+  const __nv_bfloat16* k;  // [B][H][T][d]
+  const __nv_bfloat16* v;  // [B][H][T][dv]
+  const __nv_bfloat16* P;  // [H][d][m]
+  uint16_t* kc;            // [B][H][cap][m]
+  float* kc_mul;           // [B][H][cap]
+  __nv_bfloat16* vc;       // [B][H][cap][dv]
+  const int* pos;          // [B] first cache row of each sequence
+  const int* count;        // [B] rows of k, v that are tokens, or NULL: all T
+  float* acc;              // optional [B][H][cap]: zeroed for the new rows
+  int* row_pos;            // optional [B][H][cap]: token position of the new rows
+  const int* token;        // [B] token position of the first new row, or NULL: pos
+  int B, H, T, d, m, dv, cap;
+};
+cudaError_t launch_append_ragged(const AppendParams& p, cudaStream_t stream);
+
+// One query per (sequence, head) against a shared prefix and the sequence's own rows.
+struct DecodeSharedParams {
+  const __nv_bfloat16* q;   // [B][H][d]
+  const __nv_bfloat16* P;   // [Hk][d][m]
+  const uint16_t* kc;       // [B][Hk][cap][m]
+  const float* kc_mul;      // [B][Hk][cap]
+  const __nv_bfloat16* v;   // [B][Hk][cap][dv]
+  const int* lens;          // [B]
+  const uint16_t* pkc;      // [Hk][pcap][m]
+  const float* pkc_mul;     // [Hk][pcap]
+  const __nv_bfloat16* pv;  // [Hk][pcap][dv]
+  __nv_bfloat16* out;       // [B][H][dv]
+  const float* acc;         // optional [B][Hk][cap]
+  float* acc_out;           // optional [B][Hk][cap]
+  int B, H, Hk, G, d, m, dv, cap, pcap, plen;
+  float qscale;             // log2(e)/sqrt(m)
+  char* ws;                 // workspace of decode_shared_workspace() bytes
+};
+size_t decode_shared_workspace(const DecodeSharedParams& p);
+cudaError_t launch_decode_shared(const DecodeSharedParams& p, cudaStream_t stream);
+
+// Eviction from the cache by accumulated attention weight.
+struct EvictParams {
+  uint16_t* kc;             // [B][H][cap][m]
+  float* kc_mul;            // [B][H][cap]
+  __nv_bfloat16* v;         // [B][H][cap][dv]
+  const float* acc;         // [B][H][cap]
+  const int* row_pos;       // [B][H][cap]
+  const int* lens;          // [B]
+  float* acc_out;
+  int* row_pos_out;
+  int* lens_out;            // [B]
+  int* src;                 // [B][H][budget]
+  int* ws;                  // per (b, h): move count, then (destination, source) pairs
+  int B, H, m, dv, cap, budget, sink, recent;
+};
+// ints of workspace per (b, h)
+__host__ __device__ inline size_t evict_stride(int cap, int budget) {
+  const long long moves = cap - budget < budget ? cap - budget : budget;
+  return 4 + 2 * static_cast<size_t>(moves > 0 ? moves : 0);
+}
+cudaError_t launch_evict(const EvictParams& p, cudaStream_t stream);
+
 }  // namespace spa

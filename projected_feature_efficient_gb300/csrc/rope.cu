@@ -1,0 +1,175 @@
+// rope.cu -- rotary positions on queries and keys, forward and gradient.
+//
+// Feature pair i of a row at position n is turned by the angle n * f_i:
+//   (a, b) -> scale * (a cos - b sin, a sin + b cos)
+// with (a, b) = features (2i, 2i+1) (interleaved) or (i, i + rot/2) (halves);
+// features from rot on pass through.  The map is orthogonal up to `scale`, so
+// its gradient is the same map with the angle negated (inverse).
+//
+// The angle never goes through floating point before it is reduced: the table
+// holds f_i / 2pi as a 64-bit fraction of a turn, and position * table wraps
+// modulo one turn exactly in integer arithmetic.  Its top 32 bits, as a signed
+// fraction, are the angle to within 2^-32 of a turn at any position (an fp32
+// product is off by 2^-24 of the angle itself: 0.06 rad at position 10^6).
+//
+// Bound by memory: every feature is read and written once.  A thread owns the
+// same vector of pairs in several heads of one token, so the sines are formed
+// once per thread and used for each of them.
+#include "kernels.cuh"
+
+namespace spa {
+namespace {
+
+constexpr int kThreads = 256;
+
+template <class T, int V>
+struct alignas(sizeof(T) * V) Vec {
+  T e[V];
+};
+
+__device__ __forceinline__ float up(float x) { return x; }
+__device__ __forceinline__ float up(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ void down(float& y, float x) { y = x; }
+__device__ __forceinline__ void down(__nv_bfloat16& y, float x) { y = __float2bfloat16_rn(x); }
+
+__device__ __forceinline__ void sincos_of(const RopeParams& p, int pair, int pos, float& s,
+                                          float& c) {
+  const unsigned long long turn =
+      static_cast<unsigned long long>(static_cast<long long>(pos)) * p.table[pair];
+  // signed fraction of a turn in [-1/2, 1/2): angle / pi = 2 * fraction
+  const float half_turns = static_cast<float>(static_cast<int>(turn >> 32)) * 0x1p-31f;
+  sincospif(half_turns, &s, &c);
+  s *= p.scale;
+  c *= p.scale;
+  if (p.inverse) s = -s;
+}
+
+// A thread's unit of a row: V elements (V/2 pairs) of an interleaved row, or V
+// elements of each half, or V elements of the tail.  LOOSE (interleaved, V = 2):
+// odd widths and strides, one feature at a time.
+template <class T, int V, bool INTER, bool LOOSE>
+__global__ void __launch_bounds__(kThreads) rope_kernel(const RopeParams p, int units, int turning,
+                                                        int per) {
+  const long long id = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x;
+  const long long token = id / units;
+  const int u = static_cast<int>(id - token * units);
+  if (token >= static_cast<long long>(p.B) * p.N) return;
+  const int b = static_cast<int>(token / p.N), n = static_cast<int>(token - static_cast<long long>(b) * p.N);
+  const int heads = p.H[0] + p.H[1];
+  const int h0 = blockIdx.y * per, h1 = min(heads, h0 + per);
+  const bool turns = u < turning;
+  constexpr int kPairs = INTER ? (V + 1) / 2 : V;
+  float s[kPairs], c[kPairs];
+  if (turns) {
+    const int pos = p.pos ? p.pos[token] : p.pos0 + n;
+#pragma unroll
+    for (int i = 0; i < kPairs; ++i) {
+      const int pair = INTER ? u * kPairs + i : u * V + i;
+      if (pair < p.rot / 2) {
+        sincos_of(p, pair, pos, s[i], c[i]);
+      } else {
+        s[i] = 0.f;
+        c[i] = 1.f;
+      }
+    }
+  }
+  const int half = p.rot / 2;
+  // first element of the unit; the tail of the half layout starts at rot
+  const int e0 = INTER ? u * V : turns ? u * V : p.rot + (u - turning) * V;
+  for (int h = h0; h < h1; ++h) {
+    const int t = h < p.H[0] ? 0 : 1;
+    const int hh = t ? h - p.H[0] : h;
+    const T* x = static_cast<const T*>(p.x[t]) + b * p.xs[t][0] + hh * p.xs[t][1] + n * p.xs[t][2] + e0;
+    T* y = static_cast<T*>(p.y[t]) + b * p.ys[t][0] + hh * p.ys[t][1] + n * p.ys[t][2] + e0;
+    using W = Vec<T, V>;
+    if (!turns && LOOSE) {
+      y[0] = x[0];
+      if (e0 + 1 < p.d) y[1] = x[1];
+    } else if (!turns) {
+      *reinterpret_cast<W*>(y) = *reinterpret_cast<const W*>(x);
+    } else if constexpr (INTER) {
+      W w;
+      if constexpr (LOOSE) {
+        w.e[0] = x[0];
+        w.e[1] = e0 + 1 < p.d ? x[1] : x[0];
+      } else {
+        w = *reinterpret_cast<const W*>(x);
+      }
+#pragma unroll
+      for (int i = 0; i < V / 2; ++i) {
+        if (u * (V / 2) + i < half) {  // a vector may end in the tail: those features stay as they are
+          const float a = up(w.e[2 * i]), bb = up(w.e[2 * i + 1]);
+          down(w.e[2 * i], a * c[i] - bb * s[i]);
+          down(w.e[2 * i + 1], a * s[i] + bb * c[i]);
+        }
+      }
+      if constexpr (LOOSE) {
+        y[0] = w.e[0];
+        if (e0 + 1 < p.d) y[1] = w.e[1];
+      } else {
+        *reinterpret_cast<W*>(y) = w;
+      }
+    } else {
+      W wa = *reinterpret_cast<const W*>(x), wb = *reinterpret_cast<const W*>(x + half);
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const float a = up(wa.e[i]), bb = up(wb.e[i]);
+        down(wa.e[i], a * c[i] - bb * s[i]);
+        down(wb.e[i], a * s[i] + bb * c[i]);
+      }
+      *reinterpret_cast<W*>(y) = wa;
+      *reinterpret_cast<W*>(y + half) = wb;
+    }
+  }
+}
+
+template <class T, int V, bool INTER, bool LOOSE = false>
+cudaError_t launch(const RopeParams& p, cudaStream_t stream) {
+  const int turning = INTER ? (p.rot + V - 1) / V : p.rot / 2 / V;
+  const int units = INTER ? (p.d + V - 1) / V : turning + (p.d - p.rot) / V;
+  const int heads = p.H[0] + p.H[1];
+  const long long threads = static_cast<long long>(p.B) * p.N * units;
+  int per = 1;
+  while (per < 8 && threads * heads / (2 * per) >= 152LL * 2048) per *= 2;
+  const dim3 grid(static_cast<unsigned>((threads + kThreads - 1) / kThreads),
+                  static_cast<unsigned>((heads + per - 1) / per));
+  rope_kernel<T, V, INTER, LOOSE><<<grid, kThreads, 0, stream>>>(p, units, turning, per);
+  return cudaGetLastError();
+}
+
+template <class T, bool INTER>
+cudaError_t launch_v(const RopeParams& p, int v, cudaStream_t stream) {
+  if constexpr (sizeof(T) == 2)
+    if (v == 8) return launch<T, 8, INTER>(p, stream);
+  if (v >= 4) return launch<T, 4, INTER>(p, stream);
+  if (v >= 2) return launch<T, 2, INTER>(p, stream);
+  if constexpr (INTER) return launch<T, 2, true, true>(p, stream);
+  return launch<T, 1, false>(p, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_rope(const RopeParams& p, cudaStream_t stream) {
+  const int size = p.bf16 ? 2 : 4;
+  // the widest vector that every address allows: rows, halves and tail
+  int v = 16 / size;
+  auto fits = [&](int w) {
+    const long long bytes = static_cast<long long>(w) * size;
+    if (p.d % w) return false;
+    if (!p.interleaved && ((p.rot / 2) % w || (p.d - p.rot) % w)) return false;
+    for (int t = 0; t < 2; ++t) {
+      if (p.H[t] == 0) continue;
+      if (reinterpret_cast<uintptr_t>(p.x[t]) % bytes || reinterpret_cast<uintptr_t>(p.y[t]) % bytes)
+        return false;
+      for (int i = 0; i < 3; ++i)
+        if (p.xs[t][i] % w || p.ys[t][i] % w) return false;
+    }
+    return true;
+  };
+  while (v > 1 && !fits(v)) v /= 2;
+  if (p.bf16) return p.interleaved ? launch_v<__nv_bfloat16, true>(p, v, stream)
+                                   : launch_v<__nv_bfloat16, false>(p, v, stream);
+  return p.interleaved ? launch_v<float, true>(p, v, stream) : launch_v<float, false>(p, v, stream);
+}
+
+}  // namespace spa

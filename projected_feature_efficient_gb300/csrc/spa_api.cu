@@ -58,6 +58,8 @@ constexpr int kEmpty = -1;  // internal: nothing to do
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
 // Shape / dtype checks shared by every forward entry point.
 int check_shape(int B, int H, int N, int d, int m, int dv, int dtype) {
   if (B < 0 || H < 0 || N < 0 || d < 0 || m < 0 || dv < 0) return SPA_ERR_SHAPE;
@@ -728,6 +730,32 @@ int topk_features(const void* x, void* y, long long rows, int d, int k, int dtyp
   return cuda_status(spa::launch_topk(tp, stream));
 }
 
+// Size checks of the shared-prefix decode.
+int check_decode_shared(int B, int H, int Hk, int plen, int d, int m, int d_v, int cap) {
+  if (B < 0 || H < 0 || Hk < 0 || plen < 0 || d < 0 || m < 0 || d_v < 0 || cap < 0)
+    return SPA_ERR_SHAPE;
+  if (static_cast<long long>(B) * H == 0) return kEmpty;
+  if (Hk == 0 || H % Hk || static_cast<long long>(B) * H > 65535) return SPA_ERR_SHAPE;
+  if (d < 1 || d > 256 || (m != 16 && m != 32 && m != 64 && m != 128) || (d_v != 64 && d_v != 128))
+    return SPA_ERR_UNSUPPORTED;
+  return SPA_OK;
+}
+
+int decode_shared_sizes(spa::DecodeSharedParams& dp, int B, int H, int Hk, int plen, int d, int m,
+                        int d_v, int cap) {
+  dp.B = B;
+  dp.H = H;
+  dp.Hk = Hk;
+  dp.G = H / Hk;
+  dp.plen = plen;
+  dp.d = d;
+  dp.m = m;
+  dp.dv = d_v;
+  dp.cap = cap;
+  dp.qscale = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(m)));
+  return SPA_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -947,6 +975,273 @@ int spa_attention_decode(const void* q, const void* P, const void* kc, const flo
   const cudaError_t fe = cudaFreeAsync(dp.part, s);
   if (st) return st;
   return fe == cudaSuccess ? SPA_OK : SPA_ERR_CUDA;
+}
+
+int spa_rope_frequencies(double* inv_freq, int rot, double base, int scaling, double factor,
+                         double trained, double slow, double fast) {
+  if (!inv_freq) return SPA_ERR_NULL;
+  if (rot < 2 || rot % 2 || !(base > 0.0) || !std::isfinite(base)) return SPA_ERR_SHAPE;
+  if (scaling < SPA_ROPE_PLAIN || scaling > SPA_ROPE_RAMP) return SPA_ERR_UNSUPPORTED;
+  if (scaling != SPA_ROPE_PLAIN && (!(factor > 0.0) || !std::isfinite(factor))) return SPA_ERR_SHAPE;
+  if (scaling == SPA_ROPE_BASE && rot < 4) return SPA_ERR_SHAPE;
+  if (scaling == SPA_ROPE_RAMP &&
+      (!(trained > 0.0) || !(slow >= 0.0) || !(fast > slow) || !std::isfinite(fast)))
+    return SPA_ERR_SHAPE;
+  if (scaling == SPA_ROPE_BASE) base *= std::pow(factor, static_cast<double>(rot) / (rot - 2));
+  for (int i = 0; i < rot / 2; ++i) {
+    const double f = std::pow(base, -2.0 * i / rot);
+    inv_freq[i] = f;
+    if (scaling == SPA_ROPE_LINEAR) inv_freq[i] = f / factor;
+    if (scaling == SPA_ROPE_RAMP) {
+      const double turns = trained * f / 6.283185307179586476925;
+      const double keep = turns >= fast ? 1.0 : turns <= slow ? 0.0 : (turns - slow) / (fast - slow);
+      inv_freq[i] = keep * f + (1.0 - keep) * f / factor;
+    }
+  }
+  return SPA_OK;
+}
+
+int spa_rope_table(const double* inv_freq, int rot, unsigned long long* table) {
+  if (!inv_freq || !table) return SPA_ERR_NULL;
+  if (rot < 2 || rot % 2) return SPA_ERR_SHAPE;
+  for (int i = 0; i < rot / 2; ++i)
+    if (!std::isfinite(inv_freq[i])) return SPA_ERR_SHAPE;
+  for (int i = 0; i < rot / 2; ++i) {
+    // whole turns per position drop out; the rest is at most half a turn
+    const double turns = inv_freq[i] / 6.283185307179586476925;
+    const double part = std::nearbyint((turns - std::nearbyint(turns)) * 18446744073709551616.0);
+    table[i] = part >= 9223372036854775808.0
+                   ? 0x8000000000000000ull
+                   : static_cast<unsigned long long>(static_cast<long long>(part));
+  }
+  return SPA_OK;
+}
+
+int spa_rope(const void* q, const void* k, void* q_out, void* k_out, const long long* strides,
+             const int* pos, int pos0, const unsigned long long* table, int B, int H, int Hk, int N,
+             int d, int rot, int interleaved, int inverse, float scale, int dtype, void* stream) {
+  if (B < 0 || H < 0 || Hk < 0 || N < 0 || d < 0) return SPA_ERR_SHAPE;
+  if (dtype != SPA_F32 && dtype != SPA_BF16) return SPA_ERR_DTYPE;
+  if (static_cast<long long>(B) * N == 0 || static_cast<long long>(H) + Hk == 0) return SPA_OK;
+  if (d < 1 || d > 1024) return SPA_ERR_UNSUPPORTED;
+  if (rot < 2 || rot > d || rot % 2) return SPA_ERR_SHAPE;
+  if (static_cast<long long>(H) + Hk > 65535) return SPA_ERR_SHAPE;
+  if (static_cast<long long>(B) * N > (1LL << 29)) return SPA_ERR_SHAPE;
+  if (!pos && static_cast<long long>(pos0) + N - 1 > INT_MAX) return SPA_ERR_SHAPE;
+  if (!table || (H > 0 && (!q || !q_out)) || (Hk > 0 && (!k || !k_out))) return SPA_ERR_NULL;
+  const uintptr_t es = dtype == SPA_BF16 ? 2 : 4;
+  spa::RopeParams rp{};
+  const void* in[2] = {q, k};
+  void* out[2] = {q_out, k_out};
+  const int heads[2] = {H, Hk};
+  for (int t = 0; t < 2; ++t) {
+    if (heads[t] == 0) continue;
+    if (reinterpret_cast<uintptr_t>(in[t]) % es || reinterpret_cast<uintptr_t>(out[t]) % es)
+      return SPA_ERR_ALIGN;
+    const long long dense[3] = {static_cast<long long>(heads[t]) * N * d,
+                                static_cast<long long>(N) * d, d};
+    const long long size[3] = {B, heads[t], N};
+    for (int i = 0; i < 3; ++i) {
+      rp.xs[t][i] = strides ? strides[3 * t + i] : dense[i];
+      rp.ys[t][i] = strides ? strides[6 + 3 * t + i] : dense[i];
+      // a dimension of one row is never stepped along
+      if (size[i] == 1) rp.xs[t][i] = rp.ys[t][i] = 0;
+    }
+    // the output's rows may not overlap: from the innermost dimension outwards,
+    // every step goes past all that the inner ones reach
+    long long reach = d;
+    bool used[3] = {size[0] == 1, size[1] == 1, size[2] == 1};
+    for (int left = 3 - used[0] - used[1] - used[2]; left > 0; --left) {
+      int at = -1;
+      for (int i = 0; i < 3; ++i)
+        if (!used[i] && (at < 0 || rp.ys[t][i] < rp.ys[t][at])) at = i;
+      if (rp.ys[t][at] < reach) return SPA_ERR_SHAPE;
+      if (rp.ys[t][at] > (LLONG_MAX - reach) / size[at]) return SPA_ERR_SHAPE;
+      reach += rp.ys[t][at] * (size[at] - 1);
+      used[at] = true;
+    }
+    if (in[t] == out[t])
+      for (int i = 0; i < 3; ++i)
+        if (rp.xs[t][i] != rp.ys[t][i]) return SPA_ERR_SHAPE;
+    rp.x[t] = in[t];
+    rp.y[t] = out[t];
+    rp.H[t] = heads[t];
+  }
+  if ((reinterpret_cast<uintptr_t>(table) & 7u) || (reinterpret_cast<uintptr_t>(pos) & 3u))
+    return SPA_ERR_ALIGN;
+  rp.pos = pos;
+  rp.table = table;
+  rp.B = B;
+  rp.N = N;
+  rp.d = d;
+  rp.rot = rot;
+  rp.pos0 = pos0;
+  rp.interleaved = interleaved != 0;
+  rp.inverse = inverse != 0;
+  rp.bf16 = dtype == SPA_BF16;
+  rp.scale = scale;
+  return cuda_status(spa::launch_rope(rp, static_cast<cudaStream_t>(stream)));
+}
+
+int spa_kcache_append_ragged(const void* k, const void* v, const void* P, void* kc, float* kc_mul,
+                             void* vc, const int* pos, const int* count, float* acc, int* row_pos,
+                             const int* token, int B, int H, int T, int d, int m, int d_v, int cap,
+                             int dtype, void* stream) {
+  if (B < 0 || H < 0 || T < 0 || d < 0 || m < 0 || d_v < 0 || cap < 0) return SPA_ERR_SHAPE;
+  if (dtype != SPA_F32 && dtype != SPA_BF16) return SPA_ERR_DTYPE;
+  if (B == 0 || H == 0 || T == 0 || cap == 0) return SPA_OK;
+  if (static_cast<long long>(B) * H > 65535) return SPA_ERR_SHAPE;
+  if (dtype != SPA_BF16) return SPA_ERR_UNSUPPORTED;
+  if (d < 1 || d > 256 || (m != 16 && m != 32 && m != 64 && m != 128) || (d_v != 64 && d_v != 128))
+    return SPA_ERR_UNSUPPORTED;
+  if (!k || !v || !P || !kc || !kc_mul || !vc || !pos) return SPA_ERR_NULL;
+  if (!aligned16(k) || !aligned16(v) || !aligned16(P) || !aligned16(kc) || !aligned16(vc) ||
+      !aligned4(kc_mul) || !aligned4(pos) || !aligned4(count) || !aligned4(acc) ||
+      !aligned4(row_pos) || !aligned4(token))
+    return SPA_ERR_ALIGN;
+  spa::AppendParams ap{};
+  ap.k = static_cast<const __nv_bfloat16*>(k);
+  ap.v = static_cast<const __nv_bfloat16*>(v);
+  ap.P = static_cast<const __nv_bfloat16*>(P);
+  ap.kc = static_cast<uint16_t*>(kc);
+  ap.kc_mul = kc_mul;
+  ap.vc = static_cast<__nv_bfloat16*>(vc);
+  ap.pos = pos;
+  ap.count = count;
+  ap.acc = acc;
+  ap.row_pos = row_pos;
+  ap.token = token;
+  ap.B = B;
+  ap.H = H;
+  ap.T = T;
+  ap.d = d;
+  ap.m = m;
+  ap.dv = d_v;
+  ap.cap = cap;
+  return cuda_status(spa::launch_append_ragged(ap, static_cast<cudaStream_t>(stream)));
+}
+
+int spa_attention_decode_shared_workspace_size(int B, int H, int Hk, int plen, int d, int m,
+                                               int d_v, int cap, int weights, size_t* bytes) {
+  if (!bytes) return SPA_ERR_NULL;
+  const int st = check_decode_shared(B, H, Hk, plen, d, m, d_v, cap);
+  *bytes = 0;
+  if (st == kEmpty) return SPA_OK;
+  if (st) return st;
+  spa::DecodeSharedParams dp{};
+  if (int e = decode_shared_sizes(dp, B, H, Hk, plen, d, m, d_v, cap)) return e;
+  float mark = 0.f;
+  dp.acc_out = weights ? &mark : nullptr;
+  *bytes = spa::decode_shared_workspace(dp);
+  return SPA_OK;
+}
+
+int spa_attention_decode_shared(const void* q, const void* P, const void* kc, const float* kc_mul,
+                                const void* v, const int* lens, const void* pkc,
+                                const float* pkc_mul, const void* pv, void* out, const float* acc,
+                                float* acc_out, int B, int H, int Hk, int plen, int pcap, int d,
+                                int m, int d_v, int cap, int dtype, void* workspace,
+                                size_t workspace_bytes, void* stream) {
+  if (dtype != SPA_F32 && dtype != SPA_BF16) return SPA_ERR_DTYPE;
+  int st = check_decode_shared(B, H, Hk, plen, d, m, d_v, cap);
+  if (st == kEmpty) return SPA_OK;
+  if (st) return st;
+  if (dtype != SPA_BF16) return SPA_ERR_UNSUPPORTED;
+  if (pcap < plen) return SPA_ERR_SHAPE;
+  if (!q || !P || !out) return SPA_ERR_NULL;
+  if (cap > 0 && (!kc || !kc_mul || !v || !lens)) return SPA_ERR_NULL;
+  if (plen > 0 && (!pkc || !pkc_mul || !pv)) return SPA_ERR_NULL;
+  if ((acc == nullptr) != (acc_out == nullptr)) return SPA_ERR_NULL;
+  if (!aligned16(q) || !aligned16(P) || !aligned16(kc) || !aligned16(v) || !aligned16(pkc) ||
+      !aligned16(pv) || !aligned16(out) || !aligned4(kc_mul) || !aligned4(lens) ||
+      !aligned4(pkc_mul) || !aligned4(acc) || !aligned4(acc_out) ||
+      (reinterpret_cast<uintptr_t>(workspace) & 255u))
+    return SPA_ERR_ALIGN;
+  spa::DecodeSharedParams dp{};
+  if ((st = decode_shared_sizes(dp, B, H, Hk, plen, d, m, d_v, cap))) return st;
+  dp.q = static_cast<const __nv_bfloat16*>(q);
+  dp.P = static_cast<const __nv_bfloat16*>(P);
+  dp.kc = static_cast<const uint16_t*>(kc);
+  dp.kc_mul = kc_mul;
+  dp.v = static_cast<const __nv_bfloat16*>(v);
+  dp.lens = lens;
+  dp.pkc = static_cast<const uint16_t*>(pkc);
+  dp.pkc_mul = pkc_mul;
+  dp.pv = static_cast<const __nv_bfloat16*>(pv);
+  dp.out = static_cast<__nv_bfloat16*>(out);
+  dp.acc = acc;
+  dp.acc_out = cap > 0 ? acc_out : nullptr;
+  dp.pcap = pcap;
+  const size_t need = spa::decode_shared_workspace(dp);
+  if (workspace && workspace_bytes < need) return SPA_ERR_NOMEM;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  void* own = nullptr;
+  if (!workspace)
+    if (int e = pool_alloc(&own, need, s)) return e;
+  dp.ws = static_cast<char*>(workspace ? workspace : own);
+  st = cuda_status(spa::launch_decode_shared(dp, s));
+  const cudaError_t fe = own ? cudaFreeAsync(own, s) : cudaSuccess;
+  if (st) return st;
+  return cuda_status(fe);
+}
+
+int spa_kcache_evict_workspace_size(int B, int H, int cap, int budget, size_t* bytes) {
+  if (!bytes) return SPA_ERR_NULL;
+  *bytes = 0;
+  if (B < 0 || H < 0 || cap < 0) return SPA_ERR_SHAPE;
+  if (B == 0 || H == 0 || cap == 0) return SPA_OK;
+  if (static_cast<long long>(B) * H > 65535 || budget < 1 || budget > cap) return SPA_ERR_SHAPE;
+  *bytes = align256(static_cast<size_t>(B) * H * spa::evict_stride(cap, budget) * sizeof(int));
+  return SPA_OK;
+}
+
+int spa_kcache_evict(void* kc, float* kc_mul, void* v, const float* acc, const int* row_pos,
+                     const int* lens, float* acc_out, int* row_pos_out, int* lens_out, int* src,
+                     int B, int H, int m, int d_v, int cap, int budget, int sink, int recent,
+                     void* workspace, size_t workspace_bytes, void* stream) {
+  size_t need = 0;
+  int st = spa_kcache_evict_workspace_size(B, H, cap, budget, &need);
+  if (st) return st;
+  if (need == 0) return SPA_OK;
+  if (sink < 0 || recent < 0 || static_cast<long long>(sink) + recent > budget) return SPA_ERR_SHAPE;
+  if ((m != 16 && m != 32 && m != 64 && m != 128) || (d_v != 64 && d_v != 128))
+    return SPA_ERR_UNSUPPORTED;
+  if (!kc || !kc_mul || !v || !acc || !row_pos || !lens || !acc_out || !row_pos_out || !lens_out ||
+      !src)
+    return SPA_ERR_NULL;
+  if (!aligned16(kc) || !aligned16(v) || !aligned4(kc_mul) || !aligned4(acc) ||
+      !aligned4(row_pos) || !aligned4(lens) || !aligned4(acc_out) || !aligned4(row_pos_out) ||
+      !aligned4(lens_out) || !aligned4(src) || (reinterpret_cast<uintptr_t>(workspace) & 255u))
+    return SPA_ERR_ALIGN;
+  if (workspace && workspace_bytes < need) return SPA_ERR_NOMEM;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  void* own = nullptr;
+  if (!workspace)
+    if (int e = pool_alloc(&own, need, s)) return e;
+  spa::EvictParams ep{};
+  ep.kc = static_cast<uint16_t*>(kc);
+  ep.kc_mul = kc_mul;
+  ep.v = static_cast<__nv_bfloat16*>(v);
+  ep.acc = acc;
+  ep.row_pos = row_pos;
+  ep.lens = lens;
+  ep.acc_out = acc_out;
+  ep.row_pos_out = row_pos_out;
+  ep.lens_out = lens_out;
+  ep.src = src;
+  ep.ws = static_cast<int*>(workspace ? workspace : own);
+  ep.B = B;
+  ep.H = H;
+  ep.m = m;
+  ep.dv = d_v;
+  ep.cap = cap;
+  ep.budget = budget;
+  ep.sink = sink;
+  ep.recent = recent;
+  st = cuda_status(spa::launch_evict(ep, s));
+  const cudaError_t fe = own ? cudaFreeAsync(own, s) : cudaSuccess;
+  if (st) return st;
+  return cuda_status(fe);
 }
 
 int spa_topk_features(const void* x, void* y, long long rows, int d, int k, int dtype,
