@@ -231,8 +231,19 @@ struct DecodeSharedParams {
   float qscale;             // log2(e)/sqrt(m)
   char* ws;                 // workspace of decode_shared_workspace() bytes
 };
+// What a launch needs besides: K~ and V as 3-D maps (features, rows, heads) of
+// the prefix [0] and the sequences' caches [1], with boxes of 128 and 16 rows of
+// at most 64 features; K~ fp16 in the swizzle of its box's row (32, 64 or 128
+// bytes), V bf16 in 128 bytes.
+struct DecodeSharedRun {
+  CUtensorMap k[2][2], v[2][2];
+  int sms;
+  int* err;                     // device error word
+  unsigned long long limit_ns;  // time limit of every wait in the kernel
+  int inject_stall;             // failure-detection test only: withhold one barrier arrival
+};
 size_t decode_shared_workspace(const DecodeSharedParams& p);
-cudaError_t launch_decode_shared(const DecodeSharedParams& p, cudaStream_t stream);
+cudaError_t launch_decode_shared(const DecodeSharedParams& p, const DecodeSharedRun& run, cudaStream_t stream);
 
 // Eviction from the cache by accumulated attention weight.
 struct EvictParams {

@@ -756,6 +756,54 @@ int decode_shared_sizes(spa::DecodeSharedParams& dp, int B, int H, int Hk, int p
   return SPA_OK;
 }
 
+// Rows of a cache as a 3-D tensor map with boxes of `rows` rows and at most 64
+// 16-bit features, swizzled over the box's row.
+int encode_cache_map(CUtensorMap* map, const void* base, int inner, int cap, int heads, int rows,
+                     CUtensorMapDataType type) {
+  PFN_cuTensorMapEncodeTiled_v12000 encode;
+  int st = get_encode(&encode);
+  if (st) return st;
+  const cuuint32_t width = inner < 64 ? inner : 64;
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(cap),
+                        static_cast<cuuint64_t>(heads)};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(inner) * 2, static_cast<cuuint64_t>(cap) * inner * 2};
+  cuuint32_t box[3] = {width, static_cast<cuuint32_t>(rows), 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  const CUtensorMapSwizzle swizzle = width == 16   ? CU_TENSOR_MAP_SWIZZLE_32B
+                                     : width == 32 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                                   : CU_TENSOR_MAP_SWIZZLE_128B;
+  if (encode(map, type, 3, const_cast<void*>(base), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return SPA_ERR_CUDA;
+  return SPA_OK;
+}
+
+int run_decode_shared(const spa::DecodeSharedParams& dp, cudaStream_t stream,
+                      unsigned long long limit_ns = kWaitLimitNs, int inject_stall = 0) {
+  spa::DecodeSharedRun run{};
+  int st, dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&run.sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return SPA_ERR_CUDA;
+  if ((st = device_error_ptr(&run.err))) return st;
+  for (int own = 0; own < 2; ++own) {
+    const int rows = own ? dp.cap : dp.plen, heads = own ? dp.B * dp.Hk : dp.Hk;
+    if (rows == 0) continue;  // never loaded from
+    for (int small = 0; small < 2; ++small)
+      if ((st = encode_cache_map(&run.k[own][small], own ? dp.kc : dp.pkc, dp.m,
+                                 own ? dp.cap : dp.pcap, heads, small ? 16 : 128,
+                                 CU_TENSOR_MAP_DATA_TYPE_FLOAT16)) ||
+          (st = encode_cache_map(&run.v[own][small], own ? dp.v : dp.pv, dp.dv,
+                                 own ? dp.cap : dp.pcap, heads, small ? 16 : 128,
+                                 CU_TENSOR_MAP_DATA_TYPE_BFLOAT16)))
+        return st;
+  }
+  run.limit_ns = limit_ns;
+  run.inject_stall = inject_stall;
+  return cuda_status(spa::launch_decode_shared(dp, run, stream));
+}
+
 }  // namespace
 
 extern "C" {
@@ -1179,7 +1227,7 @@ int spa_attention_decode_shared(const void* q, const void* P, const void* kc, co
   if (!workspace)
     if (int e = pool_alloc(&own, need, s)) return e;
   dp.ws = static_cast<char*>(workspace ? workspace : own);
-  st = cuda_status(spa::launch_decode_shared(dp, s));
+  st = run_decode_shared(dp, s);
   const cudaError_t fe = own ? cudaFreeAsync(own, s) : cudaSuccess;
   if (st) return st;
   return cuda_status(fe);

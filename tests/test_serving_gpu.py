@@ -15,6 +15,12 @@ BF16, F32, I32 = torch.bfloat16, torch.float32, torch.int32
 U = {BF16: 2.0 ** -8, torch.float16: 2.0 ** -11, F32: 2.0 ** -24}  # half a step
 
 
+@pytest.fixture(autouse=True)
+def no_wait_ran_out():
+    yield
+    assert spa().device_error() == 0
+
+
 def gen(seed):
     return torch.Generator(device="cuda").manual_seed(seed)
 
@@ -338,6 +344,11 @@ DECODE = [
     (2, 6, 3, 128, 64, 64, 5000, 0, [5000, 4097]),
     (1, 40, 1, 128, 128, 128, 600, 300, [555]),               # a group wider than a warp
     (1, 200, 1, 64, 32, 64, 300, 20, [290]),                  # a group wider than a tile
+    # many segments for every CTA, of one tile and of many, over several key heads
+    (16, 8, 4, 128, 32, 64, 3000, 0, [17 + 187 * i for i in range(16)]),
+    (24, 16, 8, 64, 64, 128, 700, 9000, [(97 * i) % 701 for i in range(24)]),
+    (40, 48, 4, 64, 16, 64, 520, 4000, [(131 * i) % 521 for i in range(40)]),   # and several row tiles
+    (3, 8, 4, 64, 128, 128, 4000, 20000, [4000, 1, 129]),                       # a ring of two slots
 ]
 
 
