@@ -237,11 +237,13 @@ struct DecodeSharedParams {
 // bytes), V bf16 in 128 bytes.
 struct DecodeSharedRun {
   CUtensorMap k[2][2], v[2][2];
+  CUtensorMap P;                // P (m, d, Hk), bf16, boxes of 64 rows, swizzled like K~
   int sms;
   int* err;                     // device error word
   unsigned long long limit_ns;  // time limit of every wait in the kernel
   int inject_stall;             // failure-detection test only: withhold one barrier arrival
 };
+bool decode_shared_fits(const DecodeSharedParams& p);
 size_t decode_shared_workspace(const DecodeSharedParams& p);
 cudaError_t launch_decode_shared(const DecodeSharedParams& p, const DecodeSharedRun& run, cudaStream_t stream);
 

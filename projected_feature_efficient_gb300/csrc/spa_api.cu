@@ -753,7 +753,7 @@ int decode_shared_sizes(spa::DecodeSharedParams& dp, int B, int H, int Hk, int p
   dp.dv = d_v;
   dp.cap = cap;
   dp.qscale = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(m)));
-  return SPA_OK;
+  return spa::decode_shared_fits(dp) ? SPA_OK : SPA_ERR_SHAPE;
 }
 
 // Rows of a cache as a 3-D tensor map with boxes of `rows` rows and at most 64
@@ -799,6 +799,8 @@ int run_decode_shared(const spa::DecodeSharedParams& dp, cudaStream_t stream,
                                  CU_TENSOR_MAP_DATA_TYPE_BFLOAT16)))
         return st;
   }
+  if ((st = encode_cache_map(&run.P, dp.P, dp.m, dp.d, dp.Hk, 64, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16)))
+    return st;
   run.limit_ns = limit_ns;
   run.inject_stall = inject_stall;
   return cuda_status(spa::launch_decode_shared(dp, run, stream));
