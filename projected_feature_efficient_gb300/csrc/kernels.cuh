@@ -237,7 +237,6 @@ struct DecodeSharedParams {
 // bytes), V bf16 in 128 bytes.
 struct DecodeSharedRun {
   CUtensorMap k[2][2], v[2][2];
-  CUtensorMap P;                // P (m, d, Hk), bf16, boxes of 64 rows, swizzled like K~
   int sms;
   int* err;                     // device error word
   unsigned long long limit_ns;  // time limit of every wait in the kernel

@@ -799,8 +799,6 @@ int run_decode_shared(const spa::DecodeSharedParams& dp, cudaStream_t stream,
                                  CU_TENSOR_MAP_DATA_TYPE_BFLOAT16)))
         return st;
   }
-  if ((st = encode_cache_map(&run.P, dp.P, dp.m, dp.d, dp.Hk, 64, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16)))
-    return st;
   run.limit_ns = limit_ns;
   run.inject_stall = inject_stall;
   return cuda_status(spa::launch_decode_shared(dp, run, stream));
