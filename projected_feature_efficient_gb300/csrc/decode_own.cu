@@ -74,29 +74,46 @@ __global__ void __launch_bounds__(kQueryThreads) decode_query_kernel(const __gri
     if (b >= a.p.B || g >= a.p.G) return nullptr;
     return a.p.q + (static_cast<size_t>(b) * a.p.H + hk * a.p.G + g) * d;
   };
-  for (int i = warp; i < kQueryRows; i += kQueryThreads / 32) {
-    const __nv_bfloat16* q = query_row(r0 + i);
-    for (int k = lane; k < d; k += 32) sh.q[k][i] = q ? __bfloat162float(q[k]) : 0.f;
-  }
-  __syncthreads();
-  constexpr int kRuns = kQueryThreads / M;
+  constexpr int kRuns = kQueryThreads / M, kAhead = 16;
   const int n = tid % M, run = tid / M, len = (d + kRuns - 1) / kRuns;
   const int k0 = min(run * len, d), k1 = min(k0 + len, d);
   const __nv_bfloat16* P = a.p.P + static_cast<size_t>(hk) * d * M + n;
+  __nv_bfloat16 p[kAhead];  // in flight together with the queries
+#pragma unroll
+  for (int u = 0; u < kAhead; ++u)
+    p[u] = k0 + u < k1 ? P[(k0 + u) * M] : __float2bfloat16_rn(0.f);
+  {
+    // thread = (row, every 16th feature): neighbours write neighbouring rows
+    const int i = tid % kQueryRows;
+    const __nv_bfloat16* q = query_row(r0 + i);
+#pragma unroll 8
+    for (int k = tid / kQueryRows; k < d; k += kQueryThreads / kQueryRows)
+      sh.q[k][i] = q ? __bfloat162float(q[k]) : 0.f;
+  }
+  __syncthreads();
   float acc[kQueryRows];
 #pragma unroll
   for (int r = 0; r < kQueryRows; ++r) acc[r] = 0.f;
-#pragma unroll 8
-  for (int k = k0; k < k1; ++k) {
-    const float p = __bfloat162float(P[static_cast<size_t>(k) * M]);
-    const float4* q = reinterpret_cast<const float4*>(sh.q[k]);
+#pragma unroll 1
+  for (int kb = k0; kb < k1; kb += kAhead) {
+    float f[kAhead];
 #pragma unroll
-    for (int r = 0; r < kQueryRows / 4; ++r) {
-      const float4 x = q[r];
-      acc[4 * r] = fmaf(x.x, p, acc[4 * r]);
-      acc[4 * r + 1] = fmaf(x.y, p, acc[4 * r + 1]);
-      acc[4 * r + 2] = fmaf(x.z, p, acc[4 * r + 2]);
-      acc[4 * r + 3] = fmaf(x.w, p, acc[4 * r + 3]);
+    for (int u = 0; u < kAhead; ++u) f[u] = __bfloat162float(p[u]);
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u)
+      p[u] = kb + kAhead + u < k1 ? P[(kb + kAhead + u) * M] : __float2bfloat16_rn(0.f);
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      if (kb + u >= k1) break;
+      const float4* q = reinterpret_cast<const float4*>(sh.q[kb + u]);
+#pragma unroll
+      for (int r = 0; r < kQueryRows / 4; ++r) {
+        const float4 x = q[r];
+        acc[4 * r] = fmaf(x.x, f[u], acc[4 * r]);
+        acc[4 * r + 1] = fmaf(x.y, f[u], acc[4 * r + 1]);
+        acc[4 * r + 2] = fmaf(x.z, f[u], acc[4 * r + 2]);
+        acc[4 * r + 3] = fmaf(x.w, f[u], acc[4 * r + 3]);
+      }
     }
   }
   __syncthreads();  // the runs' sums lie where the queries were

@@ -364,6 +364,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float top = warp_max(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])));
         const float scale = top > 0.f ? top : 1.f, inv = 1.f / scale;
         if (!__all_sync(0xffffffffu, wait_or_abort(&sh.kv_full[slot], (i / ST) & 1, ctl))) break;
+        // the lanes' rows lie 32, 64 or 128 bytes apart: each starts at another piece of
+        // its row, so that they meet all banks
+        const int turn = M >= 64 ? lane & 7 : M == 32 ? (lane >> 1) & 3 : (lane >> 2) & 1;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           const float f = x[c] * inv;
@@ -376,7 +379,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               uint4* at = reinterpret_cast<uint4*>(row + box * 16384);
               uint4 v[kBatch];
 #pragma unroll
-              for (int e = 0; e < kBatch; ++e) v[e] = at[e];
+              for (int e = 0; e < kBatch; ++e) v[e] = at[e ^ turn];
 #pragma unroll
               for (int e = 0; e < kBatch; ++e) {
                 __half2* u = reinterpret_cast<__half2*>(&v[e]);
@@ -384,7 +387,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int k = 0; k < 4; ++k) u[k] = __hmul2(u[k], h);
               }
 #pragma unroll
-              for (int e = 0; e < kBatch; ++e) at[e] = v[e];
+              for (int e = 0; e < kBatch; ++e) at[e ^ turn] = v[e];
             }
           }
         }
