@@ -398,11 +398,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++i;
       }
       asm volatile("cp.async.wait_all;" ::: "memory");
-    } else {
+    } else if (elect_one_sync()) {
       // ----------------------------------------------------------- MMA issue
-      // The whole warp runs the role, converged and on votes alone, and elects
-      // the issuing lane: descriptors then stay in uniform registers.  (Issued
-      // by one lane of a diverged warp, each MMA took about 200 cycles.)
+      // One elected thread; scores run two tiles ahead of the value products.
       constexpr uint32_t kIdS = idesc_f16(128, 128, kFmtF16, 0, 0);
       constexpr uint32_t kIdPV = idesc_f16(128, DV, kFmtBF16, 0, 1);
       // rows as TMA left them: 32-, 64- or 128-byte swizzle by their width
@@ -414,128 +412,93 @@ __global__ void __launch_bounds__(kThreads, 1)
       int nq = 0;                       // row tiles so far
       int nd0 = 0, nd1 = 0;             // segments finished by each stream
       int pend0 = 0, pend1 = 0;         // the streams' pending tiles: keys | first << 8 | last << 9
-      bool held = false, newq = false, more = false;
-      auto ready = [&](uint64_t* bar, uint32_t parity) {
-        return __all_sync(0xffffffffu, mbar_test_wait(bar, parity)) != 0;
-      };
-      auto wait = [&](uint64_t* bar, uint32_t parity) {
-        return __all_sync(0xffffffffu, wait_or_abort(bar, parity, ctl)) != 0;
-      };
-      auto next_seg = [&]() {
-        more = segs.next_warp(sh, ctl, s, ok);
-        more = __any_sync(0xffffffffu, more) != 0;
-        ok = __all_sync(0xffffffffu, ok) != 0;
-        newq = __any_sync(0xffffffffu, more && s.qnew) != 0;
-      };
+      int sslot = 0, sphase = 0, pslot = 0;  // ring places of is and ip
       // the q~ tile of the next segment's rows
       auto load_q = [&]() -> bool {
         if (nq > 0) {  // the old one has been read
-          if (elect_one_sync()) mma_commit(&sh.q_empty);
-          __syncwarp();
-          if (!wait(&sh.q_empty, (nq - 1) & 1)) return false;
+          mma_commit(&sh.q_empty);
+          if (!wait_or_abort(&sh.q_empty, (nq - 1) & 1, ctl)) return false;
         }
-        if (elect_one_sync()) {
-          mbar_arrive_expect_tx(&sh.q_full, P::kQBytes);
-          bulk_g2s(smem + P::kQ, a.w.qt + (static_cast<size_t>(s.hk) * a.g.RT + s.rt) * (kTile * 2 * M), P::kQBytes,
-                   &sh.q_full);
-        }
-        __syncwarp();
+        mbar_arrive_expect_tx(&sh.q_full, P::kQBytes);
+        bulk_g2s(smem + P::kQ, a.w.qt + (static_cast<size_t>(s.hk) * a.g.RT + s.rt) * (kTile * 2 * M), P::kQBytes,
+                 &sh.q_full);
         // its own copy: waited for even where another role has given up
-        if (!__all_sync(0xffffffffu, mbar_wait(&sh.q_full, nq & 1, ctl.limit_ns))) {
-          if (lane == 0) {
-            sh.abort = 1;
-            atomicExch(a.err, 1);
-          }
+        if (!mbar_wait(&sh.q_full, nq & 1, ctl.limit_ns)) {
+          sh.abort = 1;
+          atomicExch(a.err, 1);
           return false;
         }
         ++nq;
         return true;
       };
       wait_for_previous();
-      next_seg();
-      uint64_t idle = 0;
-      while (ok && (more || ip < is)) {
-        bool did = false;
-        // a new row tile waits until the value products of the old one are on their way
-        if (more && (newq ? is == ip : is < ip + 2)) {
-          const int slot = is % ST, t = is & 1;
-          const uint32_t d = tb + P::kColS + t * 128;
+      bool more = segs.next(sh, ctl, s, ok), newq = more && s.qnew;
+      while (ok) {
+        // A new row tile waits until the value products of the old one are on
+        // their way; with a ring of two slots a tile that has not landed does not
+        // hold up the value product that frees its slot's neighbour.
+        if (more && (newq ? is == ip : is < ip + 2) &&
+            (ST > 2 || is == ip || mbar_test_wait(&sh.mul_full[sslot], sphase))) {
           if (newq) {
             if (!(ok = load_q())) break;
             newq = false;
           }
-          if (ready(&sh.kv_full[slot], (is / ST) & 1) && ready(&sh.mul_full[slot], (is / ST) & 1)) {
-            tc_fence_after();
-            const uint64_t kb = k0d + static_cast<uint64_t>(slot * (P::kSlot >> 4));
-            // a failure-detection test withholds the first "scores ready"
-            const bool tell = !(a.inject_stall && !held);
-            if (elect_one_sync()) {
+          const int t = is & 1;
+          if (!(ok = wait_or_abort(&sh.mul_full[sslot], sphase, ctl) && wait_or_abort(&sh.kv_full[sslot], sphase, ctl)))
+            break;
+          tc_fence_after();
+          const uint32_t d = tb + P::kColS + t * 128;
+          const uint64_t kb = k0d + static_cast<uint64_t>(sslot * (P::kSlot >> 4));
 #pragma unroll
-              for (int k = 0; k < 2 * M / 16; ++k) {  // high parts, then low parts of q~
-                const int kk = k % (M / 16);
-                mma_ss(d, qa + (k * 4096 >> 4), kb + (((kk >> 2) * 16384 + (kk & 3) * 32) >> 4), kIdS, k > 0);
-              }
-              if (tell) mma_commit(&sh.s_full[t]);
-            }
-            __syncwarp();
-            held = true;
-            const int what = __shfl_sync(0xffffffffu, min(kTile, s.keys - j * kTile) | (j < 2) << 8 |
-                                                          (j + 2 >= s.tiles) << 9, 0);
-            if (t) pend1 = what; else pend0 = what;
-            ++is;
-            ++j;
-            if (__any_sync(0xffffffffu, j == s.tiles)) {
-              j = 0;
-              next_seg();
-            }
-            did = true;
+          for (int k = 0; k < 2 * M / 16; ++k) {  // high parts, then low parts of q~
+            const int kk = k % (M / 16);
+            mma_ss(d, qa + (k * 4096 >> 4), kb + (((kk >> 2) * 16384 + (kk & 3) * 32) >> 4), kIdS, k > 0);
           }
-        }
-        if (!did && ip < is) {
-          const int slot = ip % ST, t = ip & 1, what = t ? pend1 : pend0, nd = t ? nd1 : nd0;
+          // a failure-detection test withholds the first "scores ready"
+          if (!(a.inject_stall && is == 0)) mma_commit(&sh.s_full[t]);
+          const int what = min(kTile, s.keys - j * kTile) | (j < 2) << 8 | (j + 2 >= s.tiles) << 9;
+          if (t) pend1 = what; else pend0 = what;
+          ++is;
+          if (++sslot == ST) {
+            sslot = 0;
+            sphase ^= 1;
+          }
+          if (++j == s.tiles) {
+            j = 0;
+            more = segs.next(sh, ctl, s, ok);
+            newq = more && s.qnew;
+          }
+        } else if (ip < is) {
+          const int t = ip & 1, what = t ? pend1 : pend0, nd = t ? nd1 : nd0;
           const bool first = what >> 8 & 1;
-          if (ready(&sh.p_full[t], (ip / 2) & 1) && (!first || nd == 0 || ready(&sh.o_empty[t], (nd - 1) & 1))) {
-            tc_fence_after();
-            const uint32_t pa = tb + P::kColS + t * 128, d = tb + P::kColO + t * DV;
-            const uint64_t vb = v0d + static_cast<uint64_t>(slot * (P::kSlot >> 4));
-            const int keys = what & 255;
-            if (elect_one_sync()) {
-              mma_ts(d, pa, vb, kIdPV, !first);
-              if (keys > kTile - 16) {
+          if (!(ok = wait_or_abort(&sh.p_full[t], (ip / 2) & 1, ctl) &&
+                     (!first || nd == 0 || wait_or_abort(&sh.o_empty[t], (nd - 1) & 1, ctl))))
+            break;
+          tc_fence_after();
+          const uint32_t pa = tb + P::kColS + t * 128, d = tb + P::kColO + t * DV;
+          const uint64_t vb = v0d + static_cast<uint64_t>(pslot * (P::kSlot >> 4));
+          const int keys = what & 255;
+          mma_ts(d, pa, vb, kIdPV, !first);
+          if (keys > kTile - 16) {
 #pragma unroll
-                for (int k = 1; k < 8; ++k) mma_ts(d, pa + k * 8, vb + (k * 2048 >> 4), kIdPV, 1u);
-              } else {
+            for (int k = 1; k < 8; ++k) mma_ts(d, pa + k * 8, vb + (k * 2048 >> 4), kIdPV, 1u);
+          } else {
 #pragma unroll 1
-                for (int k = 1; k * 16 < keys; ++k)
-                  mma_ts(d, pa + k * 8, vb + static_cast<uint64_t>(k * 2048 >> 4), kIdPV, 1u);
-              }
-              mma_commit(&sh.kv_empty[slot]);
-              if (what >> 9 & 1) mma_commit(&sh.o_final[t]);
-            }
-            __syncwarp();
-            if (what >> 9 & 1) {
-              if (t) ++nd1; else ++nd0;
-            }
-            ++ip;
-            did = true;
+            for (int k = 1; k * 16 < keys; ++k)
+              mma_ts(d, pa + k * 8, vb + static_cast<uint64_t>(k * 2048 >> 4), kIdPV, 1u);
           }
-        }
-        if (did) {
-          idle = 0;
-        } else if (__any_sync(0xffffffffu, sh.abort != 0)) {
-          ok = false;
-        } else if (idle == 0) {
-          idle = globaltimer();
-        } else if (__any_sync(0xffffffffu, globaltimer() - idle > ctl.limit_ns)) {
-          if (lane == 0) {
-            sh.abort = 1;
-            atomicExch(a.err, 1);
+          mma_commit(&sh.kv_empty[pslot]);
+          if (what >> 9 & 1) {
+            mma_commit(&sh.o_final[t]);
+            if (t) ++nd1; else ++nd0;
           }
-          ok = false;
+          ++ip;
+          if (++pslot == ST) pslot = 0;
+        } else {
+          break;
         }
       }
-      if (elect_one_sync()) mma_commit(&sh.drain);
-      __syncwarp();
+      mma_commit(&sh.drain);
       mbar_wait(&sh.drain, 0, ctl.limit_ns);  // own products in flight
     }
   } else if (warp >= 8) {
