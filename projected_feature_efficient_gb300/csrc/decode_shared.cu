@@ -16,11 +16,11 @@
 // Sixteen warps in four warpgroups:
 //   warps 0-3, 4-7   softmax of the tiles of even / odd number (two streams)
 //   warps 8-11       output: a finished segment's sums, both streams joined
-//   warp  12         K~ and V tiles by TMA into a ring of slots
+//   warp  12         the list of segments (the divisions and the sequences' lengths
+//                    are its work alone) and their V tiles, by TMA into a ring
 //   warp  13         tensor-memory allocation, q~ tiles, tcgen05.mma issue
-//   warp  14         the keys' multipliers: one range for the tile's K~ rows
-//   warp  15         the list of segments, a few ahead of the other roles: the
-//                    divisions and the sequences' lengths are its work alone
+//   warps 14, 15     K~ tiles, each warp every other one, by TMA into a ring of its
+//                    own: a tile's multipliers become one range for its rows
 // The streams alternate tile by tile, each with scores and sums of its own in
 // tensor memory (S0 | S1 | O0 | O1), so that the products of one run while the
 // other is exponentiated.
@@ -31,7 +31,10 @@
 // only loses bits where it is 2^14 times smaller than another, and then below
 // fp16's rounding of that one), and the tile's common factor joins the row's.
 // (With a multiplication per score instead, read from shared memory, the softmax
-// of a tile took 600 cycles more, of 2200.)
+// of a tile took 600 cycles more, of 2200.)  K~ and V have rings of their own
+// because a K~ slot is free again once the scores are formed; with both in one slot
+// the way from a free slot to scores that can be formed took 3500 cycles, and with
+// the three slots that fit at m = 64 a tile took 2300.
 // Probabilities are rounded to bf16 for the value product (2^-8 relative,
 // averaged over the keys); their sums, and the weights that are accumulated,
 // take them in fp32.
@@ -64,29 +67,29 @@ constexpr int kThreads = 512;
 constexpr uint32_t kRegSoftmax = 168, kRegOutput = 104, kRegControl = 72;
 static_assert(128 * (2 * kRegSoftmax + kRegOutput + kRegControl) <= kThreads * 128,
               "register split exceeds the launch");
-constexpr int kLoadWarp = 12, kMmaWarp = 13, kMulWarp = 14;
-constexpr int kSchedWarp = 15;
+constexpr int kLoadWarp = 12, kMmaWarp = 13;
 constexpr int kSegs = 8;               // segments the scheduler may be ahead
-constexpr int kSegReaders = 3 + 4 + 8; // loader, issuer, multipliers, output warps, softmax warps
+constexpr int kSegReaders = 1 + 2 + 4 + 8;  // issuer, multipliers, output warps, softmax warps
 constexpr float kSumLimit = 1099511627776.f;  // 2^40
-constexpr int kMaxDynSmem = 227 * 1024 - 8 * 1024;
+constexpr int kMaxDynSmem = 227 * 1024 - 9 * 1024;
 
 constexpr int cmax(int a, int b) { return a > b ? a : b; }
 
 template <int M, int DV>
 struct Plan {
   static constexpr int kKBytes = kTile * M * 2, kVBytes = kTile * DV * 2;
-  static constexpr int kSlot = kKBytes + kVBytes;
   static constexpr int kKRow = M < 64 ? M * 2 : 128;  // bytes of a K~ row in shared memory (a box)
   static constexpr int kQBytes = kTile * 4 * M;
   static constexpr int kQ = 0, kOut = kQBytes;
-  static constexpr int kRing = kOut + 4 * 4096;  // a box of 32 x 32 sums per output warp
-  static constexpr int kFit = (kMaxDynSmem - 1024 - kRing) / kSlot;
-  static constexpr int kStages = kFit > 4 ? 4 : kFit;
-  static constexpr int kBytes = kRing + kStages * kSlot + 1024;
+  static constexpr int kKs = kOut + 4 * 4096;  // a box of 32 x 32 sums per output warp
+  static constexpr int kKStages = M == 128 ? 1 : M == 64 ? 2 : 3;  // of each of the two K~ rings
+  static constexpr int kVs = kKs + 2 * kKStages * kKBytes;
+  static constexpr int kFit = (kMaxDynSmem - 1024 - kVs) / kVBytes;
+  static constexpr int kVStages = kFit > 4 ? 4 : kFit;
+  static constexpr int kBytes = kVs + kVStages * kVBytes + 1024;
   // one CTA per SM: a second one would wait in tcgen05.alloc for the 512 columns
   static constexpr int kLaunch = cmax(kBytes, 120 * 1024);
-  static_assert(kStages >= 2 && kLaunch <= kMaxDynSmem, "shared-memory plan");
+  static_assert(kVStages >= 2 && kLaunch <= kMaxDynSmem, "shared-memory plan");
   static constexpr uint32_t kColS = 0, kColO = 256;
 };
 
@@ -101,7 +104,8 @@ struct alignas(16) Seg {
 };
 
 struct Shared {
-  uint64_t kv_full[4], kv_empty[4], mul_full[4];  // mul_full: the tile's K~ rows are in one range
+  uint64_t v_full[4], v_empty[4];
+  uint64_t k_full[2][3], k_empty[2][3], k_ready[2][3];  // ready: the tile's rows are in one range
   uint64_t s_full[2], p_full[2], o_final[2], o_empty[2];
   uint64_t q_empty, q_full, drain;
   uint64_t seg_full[kSegs], seg_empty[kSegs];
@@ -109,14 +113,16 @@ struct Shared {
   volatile int abort;
   Seg seg[kSegs];
   float stat_l[2][2][kTile], stat_m[2][2][kTile];
-  float mul[4][kTile];
-  float kscale[4];
+  float mul[2][3][kTile];
+  float kscale[16];  // by the tile's number: no warp is that many tiles behind
 };
 static_assert(offsetof(Shared, seg) % 16 == 0 && alignof(Shared) >= 16, "vector loads from shared memory");
-static_assert(sizeof(Shared) <= 8 * 1024 - 256, "static shared memory");
+static_assert(sizeof(Shared) <= 9 * 1024 - 256, "static shared memory");
 
-// The scheduler warp: the CTA's segments in order, then the end.
-__device__ __forceinline__ void run_scheduler(const Params& a, Shared& sh, const WaitCtl& ctl) {
+// The CTA's segments in order, then the end: told to the other roles, then given
+// to `load`.
+template <class Load>
+__device__ __forceinline__ void run_segments(const Params& a, Shared& sh, const WaitCtl& ctl, Load load) {
   const Geo& g = a.g;
   const int lane = threadIdx.x & 31, B = a.p.B;
   int k = 0, last = -1;
@@ -132,7 +138,7 @@ __device__ __forceinline__ void run_scheduler(const Params& a, Shared& sh, const
       mbar_arrive(&sh.seg_full[slot]);
     }
     ++k;
-    return true;
+    return s.tiles == 0 || load(s);
   };
   for (int unit = blockIdx.x; unit < g.units; unit += g.grid) {
     Seg s{};
@@ -225,31 +231,24 @@ struct Segments {
 };
 
 // ------------------------------------------------------------------ loader
-template <class P, int M, int DV>
-__device__ __forceinline__ void load_tile(const Maps& maps, uint8_t* slot, uint64_t* bar, int own, int plane,
-                                          int key, int n) {
-  const CUtensorMap* km = maps.k[own];
-  const CUtensorMap* vm = maps.v[own];
-  uint8_t* kd = slot;
-  uint8_t* vd = slot + P::kKBytes;
-  constexpr int kKBoxes = M > 64 ? 2 : 1;
+// `n` rows of a tile in boxes of 64 features: one copy each, or 16 rows at a time, so
+// that nothing behind the last step of 16 is read.
+template <int FEATURES>
+__device__ __forceinline__ void load_rows(const CUtensorMap* maps, uint8_t* to, uint64_t* bar, int plane, int key,
+                                          int n) {
+  constexpr int kBoxes = (FEATURES + 63) / 64, kRow = FEATURES < 64 ? FEATURES * 2 : 128;
   if (n == kTile) {
-    mbar_arrive_expect_tx(bar, P::kSlot);
+    mbar_arrive_expect_tx(bar, kTile * FEATURES * 2);
 #pragma unroll
-    for (int h = 0; h < kKBoxes; ++h) tma_load_3d(kd + h * 16384, &km[0], h * 64, key, plane, bar);
-#pragma unroll
-    for (int h = 0; h < DV / 64; ++h) tma_load_3d(vd + h * 16384, &vm[0], h * 64, key, plane, bar);
-  } else {  // 16 rows at a time: nothing behind the last step is read
+    for (int h = 0; h < kBoxes; ++h) tma_load_3d(to + h * 16384, &maps[0], h * 64, key, plane, bar);
+  } else {
     const int steps = (n + 15) / 16;
-    mbar_arrive_expect_tx(bar, steps * 16 * 2 * (M + DV));
-    for (int s = 0; s < steps; ++s) {
+    mbar_arrive_expect_tx(bar, steps * 16 * FEATURES * 2);
+#pragma unroll 1
+    for (int s = 0; s < steps; ++s)
 #pragma unroll
-      for (int h = 0; h < kKBoxes; ++h)
-        tma_load_3d(kd + h * 16384 + s * 16 * P::kKRow, &km[1], h * 64, key + 16 * s, plane, bar);
-#pragma unroll
-      for (int h = 0; h < DV / 64; ++h)
-        tma_load_3d(vd + h * 16384 + s * 2048, &vm[1], h * 64, key + 16 * s, plane, bar);
-    }
+      for (int h = 0; h < kBoxes; ++h)
+        tma_load_3d(to + h * 16384 + s * 16 * kRow, &maps[1], h * 64, key + 16 * s, plane, bar);
   }
 }
 
@@ -257,7 +256,7 @@ template <int M, int DV>
 __global__ void __launch_bounds__(kThreads, 1)
     decode_prefix_kernel(const __grid_constant__ Params a, const __grid_constant__ Maps maps) {
   using P = Plan<M, DV>;
-  constexpr int ST = P::kStages;
+  constexpr int VS = P::kVStages, KS = P::kKStages;
   extern __shared__ uint8_t smem_raw[];
   __shared__ Shared sh;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -270,10 +269,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_relinquish();
   }
   if (tid == 0) {
-    for (int s = 0; s < ST; ++s) {
-      mbar_init(&sh.kv_full[s], 1);
-      mbar_init(&sh.kv_empty[s], 1);
-      mbar_init(&sh.mul_full[s], 1);
+    for (int s = 0; s < VS; ++s) {
+      mbar_init(&sh.v_full[s], 1);
+      mbar_init(&sh.v_empty[s], 1);
+    }
+    for (int s = 0; s < 2 * KS; ++s) {
+      mbar_init(&sh.k_full[s / KS][s % KS], 1);
+      mbar_init(&sh.k_empty[s / KS][s % KS], 1);
+      mbar_init(&sh.k_ready[s / KS][s % KS], 1);
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(&sh.s_full[t], 1);
@@ -301,69 +304,102 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp >= 12) {
     setmaxnreg_dec<kRegControl>();
-    if (warp == kSchedWarp) {
-      run_scheduler(a, sh, ctl);
-    } else if (warp == kLoadWarp) {
+    if (warp == kLoadWarp) {
       // -------------------------------------------------------------- loader
-      if (elect_one_sync()) {
-        int i = 0;
-        while (segs.next(sh, ctl, s, ok)) {
-          for (int j = 0; j < s.tiles; ++j, ++i) {
-            const int slot = i % ST;
-            if (i >= ST && !(ok = wait_or_abort(&sh.kv_empty[slot], (i / ST - 1) & 1, ctl))) break;
-            load_tile<P, M, DV>(maps, smem + P::kRing + slot * P::kSlot, &sh.kv_full[slot], s.own, s.plane,
-                                s.key0 + j * kTile, min(kTile, s.keys - j * kTile));
+      int i = 0;
+      run_segments(a, sh, ctl, [&](const Seg& x) -> bool {
+        bool good = true;
+        if (elect_one_sync()) {
+          for (int j = 0; j < x.tiles; ++j, ++i) {
+            const int slot = i % VS;
+            if (i >= VS && !(good = wait_or_abort(&sh.v_empty[slot], (i / VS - 1) & 1, ctl))) break;
+            load_rows<DV>(maps.v[x.own], smem + P::kVs + slot * P::kVBytes, &sh.v_full[slot], x.plane,
+                          x.key0 + j * kTile, min(kTile, x.keys - j * kTile));
           }
-          if (!ok) break;
         }
-        // every copy that was started lands before the memory is given up
-        for (int k = max(0, i - ST); k < i; ++k) mbar_wait(&sh.kv_full[k % ST], (k / ST) & 1, ctl.limit_ns);
-      }
-    } else if (warp == kMulWarp) {
-      // -------------------------------------------------- keys' multipliers
-      // Copied two tiles ahead, by copies that a fence does not wait for (loads in
-      // flight at the fence below cost each tile their latency).
-      const float* from = nullptr;
-      int j = 0, i = 0, issued = 0;
-      bool more = segs.next_warp(sh, ctl, s, ok);
-      auto fetch = [&]() {
-        if (more) {
-          if (j == 0)
-            from = s.own ? a.p.kc_mul + static_cast<size_t>(s.plane) * a.p.cap + s.key0
-                         : a.p.pkc_mul + static_cast<size_t>(s.plane) * a.p.pcap + s.key0;
-          const int n = s.keys - j * kTile;
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const int k = lane + 32 * c;
-            float* to = &sh.mul[issued % 4][k];
-            if (k < n)
-              asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(to)), "l"(from + j * kTile + k)
-                           : "memory");
-            else
-              *to = 0.f;
+        return __all_sync(0xffffffffu, good);
+      });
+      // every copy that was started lands before the memory is given up (i: the
+      // elected lane knows how far it came)
+      for (int k = max(0, i - VS); k < i; ++k) mbar_wait(&sh.v_full[k % VS], (k / VS) & 1, ctl.limit_ns);
+    } else if (warp != kMmaWarp) {
+      // ---------------------------------------------------------- K~ tiles
+      // The multipliers come by copies that a fence does not wait for (loads in flight
+      // at the fence below cost each tile their latency).
+      const int mine = warp & 1;
+      uint8_t* const ring = smem + P::kKs + mine * KS * P::kKBytes;
+      int j = 0, at = 0, done = 0, issued = 0;  // tile in its segment and in all, own tiles finished and copied
+      bool end = false, between = true;         // in front of a segment
+      // Starts the next own tile's copies.  Where that needs a segment that is not
+      // told yet, or a slot, it only waits if it must: others may wait for tiles that
+      // this warp has not finished.
+      auto fetch = [&](bool must) -> bool {
+        while (!end) {
+          if (between) {
+            if (!must && !__all_sync(0xffffffffu, mbar_test_wait(&sh.seg_full[segs.k % kSegs], (segs.k / kSegs) & 1)))
+              return false;
+            end = !segs.next_warp(sh, ctl, s, ok);
+            between = false;
+            continue;
           }
-          ++issued;
+          const bool own_tile = (at & 1) == mine;
+          if (own_tile) {
+            const int slot = issued % KS;
+            if (issued >= KS) {
+              uint64_t* bar = &sh.k_empty[mine][slot];
+              const uint32_t parity = (issued / KS - 1) & 1;
+              if (must) {
+                ok = __all_sync(0xffffffffu, wait_or_abort(bar, parity, ctl));
+                if (!ok) return false;
+              } else if (!__all_sync(0xffffffffu, mbar_test_wait(bar, parity))) {
+                return false;
+              }
+            }
+            const int key = s.key0 + j * kTile, n = s.keys - j * kTile;
+            if (elect_one_sync())
+              load_rows<M>(maps.k[s.own], ring + slot * P::kKBytes, &sh.k_full[mine][slot], s.plane, key, min(kTile, n));
+            __syncwarp();
+            const float* from = (s.own ? a.p.kc_mul : a.p.pkc_mul) +
+                                static_cast<size_t>(s.plane) * (s.own ? a.p.cap : a.p.pcap) + key;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              const int k = lane + 32 * c;
+              float* to = &sh.mul[mine][slot][k];
+              if (k < n)
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(to)), "l"(from + k) : "memory");
+              else
+                *to = 0.f;
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+            ++issued;
+          }
+          ++at;
           if (++j == s.tiles) {
             j = 0;
-            more = segs.next_warp(sh, ctl, s, ok);
+            between = true;
           }
+          if (own_tile) return true;
         }
-        asm volatile("cp.async.commit_group;" ::: "memory");
+        return false;
       };
-      fetch();
-      fetch();
-      while (ok) {
-        fetch();
-        if (i == issued) break;
-        asm volatile("cp.async.wait_group 2;" ::: "memory");
+      for (;; ++done) {
+        if (issued == done && !fetch(true)) break;
+        while (issued < done + KS && fetch(false)) {
+        }
+        const int slot = done % KS;
+        if (issued == done + 3)
+          asm volatile("cp.async.wait_group 2;" ::: "memory");
+        else if (issued == done + 2)
+          asm volatile("cp.async.wait_group 1;" ::: "memory");
+        else
+          asm volatile("cp.async.wait_group 0;" ::: "memory");
         float x[4];  // each lane reads what it copied
 #pragma unroll
-        for (int c = 0; c < 4; ++c) x[c] = sh.mul[i % 4][lane + 32 * c];
-        const int slot = i % ST;
+        for (int c = 0; c < 4; ++c) x[c] = sh.mul[mine][slot][lane + 32 * c];
         // rows behind the length have the multiplier 0 here; 1 where there is none
         const float top = warp_max(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])));
-        const float scale = top > 0.f ? top : 1.f, inv = 1.f / scale;
-        if (!__all_sync(0xffffffffu, wait_or_abort(&sh.kv_full[slot], (i / ST) & 1, ctl))) break;
+        const float scale = top > 0.f ? top : 1.f, inv = __frcp_rn(scale);
+        if (!__all_sync(0xffffffffu, wait_or_abort(&sh.k_full[mine][slot], (done / KS) & 1, ctl))) break;
         // the lanes' rows lie 32, 64 or 128 bytes apart: each starts at another piece of
         // its row, so that they meet all banks
         const int turn = M >= 64 ? lane & 7 : M == 32 ? (lane >> 1) & 3 : (lane >> 2) & 1;
@@ -372,14 +408,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float f = x[c] * inv;
           if (__any_sync(0xffffffffu, f != 1.f)) {  // row lane + 32 c, all of it by one factor
             const __half2 h = __float2half2_rn(f);
-            uint8_t* row = smem + P::kRing + slot * P::kSlot + (lane + 32 * c) * P::kKRow;
+            uint8_t* row = ring + slot * P::kKBytes + (lane + 32 * c) * P::kKRow;
             constexpr int kBatch = M / 8 < 8 ? M / 8 : 8;  // 16-byte pieces in flight
 #pragma unroll 1
             for (int box = 0; box < M / 8 / kBatch; ++box) {
-              uint4* at = reinterpret_cast<uint4*>(row + box * 16384);
+              uint4* w = reinterpret_cast<uint4*>(row + box * 16384);
               uint4 v[kBatch];
 #pragma unroll
-              for (int e = 0; e < kBatch; ++e) v[e] = at[e ^ turn];
+              for (int e = 0; e < kBatch; ++e) v[e] = w[e ^ turn];
 #pragma unroll
               for (int e = 0; e < kBatch; ++e) {
                 __half2* u = reinterpret_cast<__half2*>(&v[e]);
@@ -387,17 +423,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int k = 0; k < 4; ++k) u[k] = __hmul2(u[k], h);
               }
 #pragma unroll
-              for (int e = 0; e < kBatch; ++e) at[e ^ turn] = v[e];
+              for (int e = 0; e < kBatch; ++e) w[e ^ turn] = v[e];
             }
           }
         }
-        if (lane == 0) sh.kscale[slot] = scale;
+        if (lane == 0) sh.kscale[(2 * done + mine) % 16] = scale;
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.mul_full[slot]);
-        ++i;
+        if (lane == 0) mbar_arrive(&sh.k_ready[mine][slot]);
       }
       asm volatile("cp.async.wait_all;" ::: "memory");
+      for (int k = max(0, issued - KS); k < issued; ++k)
+        mbar_wait(&sh.k_full[mine][k % KS], (k / KS) & 1, ctl.limit_ns);
     } else if (elect_one_sync()) {
       // ----------------------------------------------------------- MMA issue
       // One elected thread; scores run two tiles ahead of the value products.
@@ -406,13 +443,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       // rows as TMA left them: 32-, 64- or 128-byte swizzle by their width
       constexpr uint32_t kLayout = M == 16 ? 6 : M == 32 ? 4 : kLayoutSwizzle128;
       const uint64_t qa = smem_desc(sbase + P::kQ, 2048, 128, kLayoutInterleave);
-      const uint64_t k0d = smem_desc(sbase + P::kRing, 16, 8 * P::kKRow, kLayout);
-      const uint64_t v0d = smem_desc(sbase + P::kRing + P::kKBytes, 16384, 1024, kLayoutSwizzle128);
+      const uint64_t k0d = smem_desc(sbase + P::kKs, 16, 8 * P::kKRow, kLayout);
+      const uint64_t v0d = smem_desc(sbase + P::kVs, 16384, 1024, kLayoutSwizzle128);
       int j = 0, is = 0, ip = 0;        // tile in its segment; next score and value products
       int nq = 0;                       // row tiles so far
       int nd0 = 0, nd1 = 0;             // segments finished by each stream
       int pend0 = 0, pend1 = 0;         // the streams' pending tiles: keys | first << 8 | last << 9
-      int sslot = 0, sphase = 0, pslot = 0;  // ring places of is and ip
+      int kslot = 0, kphase = 0, vslot = 0, vphase = 0;  // ring places of is (in its stream's ring) and ip
       // the q~ tile of the next segment's rows
       auto load_q = [&]() -> bool {
         if (nq > 0) {  // the old one has been read
@@ -434,21 +471,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       wait_for_previous();
       bool more = segs.next(sh, ctl, s, ok), newq = more && s.qnew;
       while (ok) {
-        // A new row tile waits until the value products of the old one are on
-        // their way; with a ring of two slots a tile that has not landed does not
-        // hold up the value product that frees its slot's neighbour.
-        if (more && (newq ? is == ip : is < ip + 2) &&
-            (ST > 2 || is == ip || mbar_test_wait(&sh.mul_full[sslot], sphase))) {
+        // a new row tile waits until the value products of the old one are on their way
+        if (more && (newq ? is == ip : is < ip + 2)) {
           if (newq) {
             if (!(ok = load_q())) break;
             newq = false;
           }
           const int t = is & 1;
-          if (!(ok = wait_or_abort(&sh.mul_full[sslot], sphase, ctl) && wait_or_abort(&sh.kv_full[sslot], sphase, ctl)))
-            break;
+          if (!(ok = wait_or_abort(&sh.k_ready[t][kslot], kphase, ctl))) break;
           tc_fence_after();
           const uint32_t d = tb + P::kColS + t * 128;
-          const uint64_t kb = k0d + static_cast<uint64_t>(sslot * (P::kSlot >> 4));
+          const uint64_t kb = k0d + static_cast<uint64_t>((t * KS + kslot) * (P::kKBytes >> 4));
 #pragma unroll
           for (int k = 0; k < 2 * M / 16; ++k) {  // high parts, then low parts of q~
             const int kk = k % (M / 16);
@@ -456,12 +489,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           // a failure-detection test withholds the first "scores ready"
           if (!(a.inject_stall && is == 0)) mma_commit(&sh.s_full[t]);
+          mma_commit(&sh.k_empty[t][kslot]);
           const int what = min(kTile, s.keys - j * kTile) | (j < 2) << 8 | (j + 2 >= s.tiles) << 9;
           if (t) pend1 = what; else pend0 = what;
-          ++is;
-          if (++sslot == ST) {
-            sslot = 0;
-            sphase ^= 1;
+          if ((++is & 1) == 0 && ++kslot == KS) {
+            kslot = 0;
+            kphase ^= 1;
           }
           if (++j == s.tiles) {
             j = 0;
@@ -471,12 +504,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else if (ip < is) {
           const int t = ip & 1, what = t ? pend1 : pend0, nd = t ? nd1 : nd0;
           const bool first = what >> 8 & 1;
-          if (!(ok = wait_or_abort(&sh.p_full[t], (ip / 2) & 1, ctl) &&
+          if (!(ok = wait_or_abort(&sh.p_full[t], (ip / 2) & 1, ctl) && wait_or_abort(&sh.v_full[vslot], vphase, ctl) &&
                      (!first || nd == 0 || wait_or_abort(&sh.o_empty[t], (nd - 1) & 1, ctl))))
             break;
           tc_fence_after();
           const uint32_t pa = tb + P::kColS + t * 128, d = tb + P::kColO + t * DV;
-          const uint64_t vb = v0d + static_cast<uint64_t>(pslot * (P::kSlot >> 4));
+          const uint64_t vb = v0d + static_cast<uint64_t>(vslot * (P::kVBytes >> 4));
           const int keys = what & 255;
           mma_ts(d, pa, vb, kIdPV, !first);
           if (keys > kTile - 16) {
@@ -487,13 +520,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int k = 1; k * 16 < keys; ++k)
               mma_ts(d, pa + k * 8, vb + static_cast<uint64_t>(k * 2048 >> 4), kIdPV, 1u);
           }
-          mma_commit(&sh.kv_empty[pslot]);
+          mma_commit(&sh.v_empty[vslot]);
           if (what >> 9 & 1) {
             mma_commit(&sh.o_final[t]);
             if (t) ++nd1; else ++nd0;
           }
           ++ip;
-          if (++pslot == ST) pslot = 0;
+          if (++vslot == VS) {
+            vslot = 0;
+            vphase ^= 1;
+          }
         } else {
           break;
         }
@@ -594,11 +630,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         srow = a.w.scores + static_cast<size_t>(s.srow + r) * a.g.capr + s.key0;
 #pragma unroll 1
       for (; at < i1; at += 2) {
-        const int j = at - i, n = min(kTile, s.keys - j * kTile), slot = at % ST;
+        const int j = at - i, n = min(kTile, s.keys - j * kTile);
         if (!(ok = __all_sync(0xffffffffu, wait_or_abort(&sh.s_full[t], (at / 2) & 1, ctl)))) break;
         tc_fence_after();
         if (n & 15) {  // value rows up to the next step of 16: zero
-          uint8_t* vd = smem + P::kRing + slot * P::kSlot + P::kKBytes;
+          if (!(ok = __all_sync(0xffffffffu, wait_or_abort(&sh.v_full[at % VS], (at / VS) & 1, ctl)))) break;
+          uint8_t* vd = smem + P::kVs + at % VS * P::kVBytes;
           const int words = (16 - (n & 15)) * (DV / 8);
 #pragma unroll 1
           for (int c = r; c < words; c += 128) {
@@ -625,7 +662,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               x[96 + c] = __uint_as_float(v3[c]);
             }
           }
-          const float mult = qm * sh.kscale[slot];  // > 0
+          const float mult = qm * sh.kscale[at % 16];  // > 0
           if (n < kTile) {
 #pragma unroll
             for (int c = 0; c < 128; ++c) x[c] = c < n ? x[c] : -INFINITY;
