@@ -436,7 +436,8 @@ SPA_API int spa_attention_decode_shared(const void *q, const void *P, const void
  *     src                       [B][H][budget] the row that each row was
  *                               before, -1 behind the new length
  *   1 <= budget <= cap, sink, recent >= 0, sink + recent <= budget, else
- *   SPA_ERR_SHAPE; m, d_v as above, B*H <= 65535.  workspace as above.
+ *   SPA_ERR_SHAPE; m, d_v as above, cap <= 2^20, B*H <= 65535.  workspace as
+ *   above.
  */
 SPA_API int spa_kcache_evict_workspace_size(int B, int H, int cap, int budget, size_t *bytes);
 SPA_API int spa_kcache_evict(void *kc, float *kc_mul, void *v, const float *acc,

@@ -11,17 +11,23 @@
 // Sources lie at or behind the new length and destinations in front of it: the
 // moves of all rows run at once.
 //
-//   evict_select_kernel  one CTA per (sequence, head): the weight of the last
-//                        row that stays by a radix selection (8 bits at a
-//                        time) on order-preserving 32-bit keys, then one pass
-//                        that pairs the holes with the rows to move
-//   evict_move_kernel    the rows' K~, multiplier and V, a warp per row
+//   evict_select_kernel  one CTA per (sequence, head): the weights once from
+//                        memory, as order-preserving 32-bit keys in registers (or
+//                        shared memory, by the cache's length); the key of the last
+//                        row that stays by a radix selection (or, for a few rows to
+//                        drop, those one by one); then the ranks of holes and of rows
+//                        to move, a lane per row
+//   evict_move_kernel    the rows' K~, multiplier and V, a warp per row, four rows
+//                        in flight
+// The first is bound by issued instructions, the second by memory.  Other selections
+// that were measured on 512 pairs of 2049 rows (18 us with the histogram): equal digits
+// of a warp counted by one lane 39 us, two bits per pass by counting keys above three
+// candidates 31 us.
+#include "decode_shared.cuh"
 #include "kernels.cuh"
 
 namespace spa {
 namespace {
-
-constexpr int kSelThreads = 1024;
 
 // Keys in the order of the weights: protected rows on top, NaN at the bottom.
 __device__ __forceinline__ uint32_t key_of(float w, int pos, int sink, int last) {
@@ -33,38 +39,31 @@ __device__ __forceinline__ uint32_t key_of(float w, int pos, int sink, int last)
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-// Exclusive prefix sum over the block of a small value per thread; total in *sum.
-__device__ __forceinline__ int block_scan(int v, int* red, int* sum) {
+// Counts (one per warp, the same in all its lanes) of the warps in front of this one.
+template <int THREADS>
+__device__ __forceinline__ int2 warps_before(int2 v, int2* red) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int s = v;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int t = __shfl_up_sync(0xffffffffu, s, o);
-    if (lane >= o) s += t;
-  }
-  if (lane == 31) red[warp] = s;
+  if (lane == 0) red[warp] = v;
   __syncthreads();
-  if (warp == 0) {
-    int w = red[lane];
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int t = __shfl_up_sync(0xffffffffu, w, o);
-      if (lane >= o) w += t;
-    }
-    red[lane] = w;
-  }
-  __syncthreads();
-  const int before = (warp ? red[warp - 1] : 0) + s - v;
-  *sum = red[31];
-  __syncthreads();
-  return before;
+  const int2 w = lane < warp ? red[lane] : make_int2(0, 0);
+  return make_int2(__reduce_add_sync(0xffffffffu, w.x), __reduce_add_sync(0xffffffffu, w.y));
 }
 
-__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictParams p) {
-  __shared__ int hist[256];
-  __shared__ int red[32];
-  __shared__ int sh_bin, sh_above;
-  const int bh = blockIdx.x, b = bh / p.H, tid = threadIdx.x;
+// Where the keys are between the passes.
+enum Keys { kRegisters, kShared, kNowhere };
+constexpr int kRegKeys = 16;  // rows per thread that fit in registers
+constexpr int kFew = 4;       // rows to drop that are looked for one by one
+
+template <int THREADS, Keys KEYS>
+__global__ void __launch_bounds__(THREADS) evict_select_kernel(const EvictParams p) {
+  extern __shared__ uint32_t dyn[];  // a bit per row that stays; kShared: the keys behind them
+  constexpr int W = THREADS / 32;
+  __shared__ alignas(16) int hist[2][256];
+  __shared__ uint64_t found[2][W];
+  __shared__ int red[W];
+  __shared__ int2 red2[2][W];
+  ds::let_next_start();
+  const int bh = blockIdx.x, b = bh / p.H, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int n = min(max(p.lens[b], 0), p.cap);
   const int left = min(n, p.budget);
   const float* acc = p.acc + static_cast<size_t>(bh) * p.cap;
@@ -73,9 +72,9 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
   int* pos_out = p.row_pos_out + static_cast<size_t>(bh) * p.cap;
   int* src = p.src + static_cast<size_t>(bh) * p.budget;
   int* ws = p.ws + static_cast<size_t>(bh) * evict_stride(p.cap, p.budget);
-  for (int i = left + tid; i < p.budget; i += kSelThreads) src[i] = -1;
+  for (int i = left + tid; i < p.budget; i += THREADS) src[i] = -1;
   if (n <= p.budget) {
-    for (int i = tid; i < n; i += kSelThreads) {
+    for (int i = tid; i < n; i += THREADS) {
       src[i] = i;
       if (acc_out != acc) acc_out[i] = acc[i];
       if (pos_out != pos) pos_out[i] = pos[i];
@@ -83,89 +82,207 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
     if (tid == 0) ws[0] = 0;
     return;
   }
+  // A warp takes a run of 32-row words, w0 .. w1-1, a lane a row of each.
+  const int words = (n + 31) / 32, per = (words + W - 1) / W;
+  const int w0 = min(warp * per, words), w1 = min(w0 + per, words);
+  uint32_t* const bits = dyn;
+  uint32_t* const keys = dyn + (p.cap + 31) / 32;
+  uint32_t reg[KEYS == kRegisters ? kRegKeys : 1];
+  float weight[KEYS == kRegisters ? kRegKeys : 1];
+  int last = 0;
+  // f(word, row, key) for the warp's words; a lane behind the last row has row >= n
+  auto each = [&](auto f) {
+    if constexpr (KEYS == kRegisters) {
+#pragma unroll
+      for (int e = 0; e < kRegKeys; ++e)
+        if (w0 + e < w1) f(w0 + e, 32 * (w0 + e) + lane, reg[e]);
+    } else {
+#pragma unroll 4
+      for (int w = w0; w < w1; ++w) {
+        const int i = 32 * w + lane;
+        f(w, i, i >= n ? 0u : KEYS == kShared ? keys[i] : key_of(acc[i], pos[i], p.sink, last));
+      }
+    }
+  };
   // the newest token position
   int newest = -2147483647 - 1;
-  for (int i = tid; i < n; i += kSelThreads) newest = max(newest, pos[i]);
+  if constexpr (KEYS == kRegisters) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) newest = max(newest, __shfl_xor_sync(0xffffffffu, newest, o));
-  if ((tid & 31) == 0) red[tid >> 5] = newest;
+    for (int e = 0; e < kRegKeys; ++e) {
+      const int i = 32 * (w0 + e) + lane;
+      const bool in = w0 + e < w1 && i < n;
+      const int x = in ? pos[i] : -2147483647 - 1;
+      weight[e] = in ? acc[i] : 0.f;
+      reg[e] = static_cast<uint32_t>(x);
+      newest = max(newest, x);
+    }
+  } else {
+#pragma unroll 8
+    for (int w = w0; w < w1; ++w) newest = max(newest, 32 * w + lane < n ? pos[32 * w + lane] : newest);
+  }
+  newest = __reduce_max_sync(0xffffffffu, newest);
+  if (lane == 0) red[warp] = newest;
   __syncthreads();
-  newest = red[0];
-  for (int w = 1; w < 32; ++w) newest = max(newest, red[w]);
-  __syncthreads();
+  newest = __reduce_max_sync(0xffffffffu, red[lane % W]);
   // positions above `last` are protected (in 64 bits: `recent` may reach below the lowest)
   const long long last64 = static_cast<long long>(newest) - p.recent;
-  const int last = last64 < -2147483647LL - 1 ? -2147483647 - 1 : static_cast<int>(last64);
-
-  // radix selection of the left-th largest key
-  uint32_t prefix = 0, mask = 0;
-  int want = left;  // this many keys are wanted among those that match the prefix
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    for (int i = tid; i < 256; i += kSelThreads) hist[i] = 0;
-    __syncthreads();
-    for (int i = tid; i < n; i += kSelThreads) {
-      const uint32_t k = key_of(acc[i], pos[i], p.sink, last);
-      if ((k & mask) == prefix) atomicAdd(&hist[(k >> shift) & 255u], 1);
+  last = last64 < -2147483647LL - 1 ? -2147483647 - 1 : static_cast<int>(last64);
+  if constexpr (KEYS == kRegisters) {
+#pragma unroll
+    for (int e = 0; e < kRegKeys; ++e)
+      reg[e] = w0 + e < w1 && 32 * (w0 + e) + lane < n ? key_of(weight[e], static_cast<int>(reg[e]), p.sink, last) : 0u;
+  } else if constexpr (KEYS == kShared) {
+#pragma unroll 8
+    for (int w = w0; w < w1; ++w) {
+      const int i = 32 * w + lane;
+      if (i < n) keys[i] = key_of(acc[i], pos[i], p.sink, last);  // read by this lane alone
     }
-    __syncthreads();
-    // thread t < 256 looks at bin 255 - t: how many keys lie in higher bins
-    const int c = tid < 256 ? hist[255 - tid] : 0;
-    int total;
-    const int above = block_scan(c, red, &total);
-    if (tid < 256 && above < want && above + c >= want) {
-      sh_bin = 255 - tid;
-      sh_above = above;
-    }
-    __syncthreads();
-    prefix |= static_cast<uint32_t>(sh_bin) << shift;
-    mask |= 255u << shift;
-    want -= sh_above;
-    __syncthreads();
   }
-  // keys above `prefix` stay, and the first `want` rows of those equal to it
-  int ties = 0, holes = 0, movers = 0;
-  for (int i0 = 0; i0 < n; i0 += kSelThreads) {
-    const int i = i0 + tid;
-    float a = 0.f;
-    int ps = 0;
-    uint32_t k = 0;
-    if (i < n) {
-      a = acc[i];
-      ps = pos[i];
-      k = key_of(a, ps, p.sink, last);
+  // `low` and `want`: the rows of a larger key stay, and of those equal to it the
+  // first `want` (all of them: exact = false).
+  uint32_t low = 0;
+  int want = 0;
+  bool exact = true;
+  uint32_t keep = ~0u;  // the bits that are compared
+  if (n - left <= kFew) {
+    // The usual step drops a row: the worst rows one after the other, by smallest
+    // key and then last row.  The last of them to go has the key `low`.
+    uint64_t gone = ~0ull;  // (key, row from the end) of the last one that went
+    int dropped = 0;        // of the key `low`
+    for (int round = 0; round < n - left; ++round) {
+      uint64_t worst = ~0ull;
+      each([&](int, int i, uint32_t k) {
+        const uint64_t x = static_cast<uint64_t>(k) << 32 | static_cast<uint32_t>(n - 1 - i);
+        if (i < n && x < worst && (round == 0 || x > gone)) worst = x;
+      });
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        const uint64_t x = __shfl_xor_sync(0xffffffffu, worst, o);
+        worst = x < worst ? x : worst;
+      }
+      if (lane == 0) found[round & 1][warp] = worst;
+      __syncthreads();
+      worst = found[round & 1][lane % W];
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        const uint64_t x = __shfl_xor_sync(0xffffffffu, worst, o);
+        worst = x < worst ? x : worst;
+      }
+      gone = worst;
+      const uint32_t k = static_cast<uint32_t>(worst >> 32);
+      dropped = round > 0 && k == low ? dropped + 1 : 1;
+      low = k;
     }
-    const bool tie = i < n && k == prefix;
-    int sum;
-    const int tr = ties + block_scan(tie, red, &sum);
-    ties += sum;
-    const bool kept = i < n && (k > prefix || (tie && tr < want));
-    // below the new length the places to fill are counted, behind it the rows to move
-    const bool hole = i < left && !kept, mover = i >= left && kept;
-    const int hr = holes + block_scan(hole, red, &sum);
-    holes += sum;
-    const int mr = movers + block_scan(mover, red, &sum);
-    movers += sum;
-    if (hole) ws[4 + 2 * hr] = i;
-    __syncthreads();  // the holes come before the rows that fill them
-    if (kept && i < left) {
-      src[i] = i;
-      if (acc_out != acc) acc_out[i] = a;
-      if (pos_out != pos) pos_out[i] = ps;
+    // those equal to `low` that stay: all but the last `dropped` of them
+    int same = 0;
+    each([&](int, int i, uint32_t k) { same += i < n && k == low; });
+    same = __reduce_add_sync(0xffffffffu, same);
+    if (lane == 0) red2[0][warp] = make_int2(same, 0);
+    __syncthreads();
+    want = __reduce_add_sync(0xffffffffu, lane < W ? red2[0][lane].x : 0) - dropped;
+    __syncthreads();
+  } else {
+    // radix selection of the left-th largest key, 8 bits at a time until all keys of
+    // the digit stay; below, keys are compared in the bits that were decided
+    uint32_t mask = 0;
+    int count = n;
+    want = left;
+    for (int i = tid; i < 256; i += THREADS) hist[0][i] = 0;
+    __syncthreads();
+    for (int shift = 24, turn = 0; shift >= 0; shift -= 8, turn ^= 1) {
+      each([&](int, int i, uint32_t k) {
+        if (i < n && (k & mask) == low) atomicAdd(&hist[turn][(k >> shift) & 255u], 1);
+      });
+      for (int i = tid; i < 256; i += THREADS) hist[turn ^ 1][i] = 0;
+      __syncthreads();
+      // lane l of every warp looks at the bins 255 - 8l .. 248 - 8l: how many keys lie above
+      const int4 x = reinterpret_cast<const int4*>(hist[turn])[63 - 2 * lane];
+      const int4 y = reinterpret_cast<const int4*>(hist[turn])[62 - 2 * lane];
+      const int c[8] = {x.w, x.z, x.y, x.x, y.w, y.z, y.y, y.x};
+      int sum = 0;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sum += c[e];
+      int before = sum;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int t = __shfl_up_sync(0xffffffffu, before, o);
+        if (lane >= o) before += t;
+      }
+      before -= sum;
+      const int l = __ffs(__ballot_sync(0xffffffffu, before < want && before + sum >= want)) - 1;
+      int bin = 0, rest = 0, size = 0;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        if (before < want && before + c[e] >= want) {
+          bin = 255 - 8 * lane - e;
+          rest = want - before;
+          size = c[e];
+        }
+        before += c[e];
+      }
+      low |= static_cast<uint32_t>(__shfl_sync(0xffffffffu, bin, l)) << shift;
+      mask |= 255u << shift;
+      want = __shfl_sync(0xffffffffu, rest, l);
+      count = __shfl_sync(0xffffffffu, size, l);
+      if (want == count) break;
+      __syncthreads();  // this histogram is zeroed in the next pass
     }
-    if (mover) {
-      const int to = ws[4 + 2 * mr];
-      ws[4 + 2 * mr + 1] = i;
+    exact = want < count;
+    keep = mask;
+  }
+  const uint32_t lower = (1u << lane) - 1u;
+  int ties = 0;
+  if (exact) {
+    each([&](int, int i, uint32_t k) { ties += __popc(__ballot_sync(0xffffffffu, i < n && (k & keep) == low)); });
+    ties = warps_before<THREADS>(make_int2(ties, 0), red2[0]).x;
+  }
+  int2 moves = make_int2(0, 0);  // below the new length the places to fill, behind it the rows to move
+  auto below = [&](int w) {      // rows of the word below the new length
+    const int cut = left - 32 * w;
+    return cut >= 32 ? 0xffffffffu : cut <= 0 ? 0u : (1u << cut) - 1u;
+  };
+  each([&](int w, int i, uint32_t k) {
+    k &= keep;
+    const uint32_t tie = __ballot_sync(0xffffffffu, i < n && k == low);
+    const bool stays = i < n && (k > low || (k == low && (!exact || ties + __popc(tie & lower) < want)));
+    ties += __popc(tie);
+    const uint32_t m = __ballot_sync(0xffffffffu, stays);
+    if (lane == 0) bits[w] = m;
+    moves.x += __popc(~m & below(w));
+    moves.y += __popc(m & ~below(w));
+  });
+  int2 at = warps_before<THREADS>(moves, red2[1]);
+  if (tid == THREADS - 1) ws[0] = at.x + moves.x;
+#pragma unroll 4
+  for (int w = w0; w < w1; ++w) {
+    const uint32_t holes = ~bits[w] & below(w);
+    if (holes >> lane & 1u) ws[4 + 2 * (at.x + __popc(holes & lower))] = 32 * w + lane;
+    at.x += __popc(holes);
+  }
+  __syncthreads();  // the holes come before the rows that fill them
+#pragma unroll 4
+  for (int w = w0; w < w1; ++w) {
+    const int i = 32 * w + lane;
+    const uint32_t m = bits[w], movers = m & ~below(w);
+    if (m >> lane & 1u) {
+      int to = i;
+      if (movers >> lane & 1u) {
+        int* move = ws + 4 + 2 * (at.y + __popc(movers & lower));
+        to = move[0];
+        move[1] = i;
+      }
       src[to] = i;
-      acc_out[to] = a;
-      pos_out[to] = ps;
+      if (to != i || acc_out != acc) acc_out[to] = acc[i];
+      if (to != i || pos_out != pos) pos_out[to] = pos[i];
     }
+    at.y += __popc(movers);
   }
-  if (tid == 0) ws[0] = holes;
 }
 
 constexpr int kMoveThreads = 256;
 
 __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictParams p, int blocks) {
+  ds::wait_for_previous();
   const int bh = blockIdx.x / blocks, part = blockIdx.x % blocks;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int* ws = p.ws + static_cast<size_t>(bh) * evict_stride(p.cap, p.budget);
@@ -174,11 +291,31 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictPar
   uint4* kc = reinterpret_cast<uint4*>(p.kc) + static_cast<size_t>(bh) * p.cap * kp;
   uint4* v = reinterpret_cast<uint4*>(p.v) + static_cast<size_t>(bh) * p.cap * vp;
   float* mul = p.kc_mul + static_cast<size_t>(bh) * p.cap;
-  for (int i = part * (kMoveThreads / 32) + warp; i < moves; i += blocks * (kMoveThreads / 32)) {
-    const size_t to = ws[4 + 2 * i], from = ws[4 + 2 * i + 1];
-    if (lane < kp) kc[to * kp + lane] = kc[from * kp + lane];
-    if (lane < vp) v[to * vp + lane] = v[from * vp + lane];
-    if (lane == 0) mul[to] = mul[from];
+  const int stride = blocks * (kMoveThreads / 32);
+  constexpr int E = 4;  // rows in flight
+  for (int i0 = part * (kMoveThreads / 32) + warp; i0 < moves; i0 += E * stride) {
+    int2 at[E];  // destination, source
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+      if (i0 + e * stride < moves) at[e] = *reinterpret_cast<const int2*>(ws + 4 + 2 * (i0 + e * stride));
+    uint4 a[E], c[E];
+    float f[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      if (i0 + e * stride >= moves) continue;
+      const size_t from = at[e].y;
+      if (lane < kp) a[e] = kc[from * kp + lane];
+      if (lane < vp) c[e] = v[from * vp + lane];
+      if (lane == 0) f[e] = mul[from];
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      if (i0 + e * stride >= moves) continue;
+      const size_t to = at[e].x;
+      if (lane < kp) kc[to * kp + lane] = a[e];
+      if (lane < vp) v[to * vp + lane] = c[e];
+      if (lane == 0) mul[to] = f[e];
+    }
   }
   // one thread per sequence reads its length and writes the new one
   if (part == 0 && bh % p.H == 0 && threadIdx.x == 0) {
@@ -187,15 +324,30 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictPar
   }
 }
 
+template <int THREADS, Keys KEYS>
+cudaError_t launch_select(const EvictParams& p, cudaStream_t stream) {
+  const long long words = (p.cap + 31LL) / 32;
+  const int smem = static_cast<int>(4 * (KEYS == kShared ? 33 * words : words));
+  const cudaError_t e = cudaFuncSetAttribute(evict_select_kernel<THREADS, KEYS>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  evict_select_kernel<THREADS, KEYS><<<p.B * p.H, THREADS, smem, stream>>>(p);
+  return cudaGetLastError();
+}
+
 }  // namespace
 
 cudaError_t launch_evict(const EvictParams& p, cudaStream_t stream) {
-  evict_select_kernel<<<p.B * p.H, kSelThreads, 0, stream>>>(p);
-  cudaError_t e = cudaGetLastError();
+  // the smallest CTA whose registers hold the keys; longer caches in shared memory
+  // (up to 200 KB), the longest from memory in every pass
+  cudaError_t e = p.cap <= 256 * kRegKeys    ? launch_select<256, kRegisters>(p, stream)
+                  : p.cap <= 512 * kRegKeys  ? launch_select<512, kRegisters>(p, stream)
+                  : p.cap <= 1024 * kRegKeys ? launch_select<1024, kRegisters>(p, stream)
+                  : p.cap <= 49600           ? launch_select<1024, kShared>(p, stream)
+                                             : launch_select<1024, kNowhere>(p, stream);
   if (e != cudaSuccess) return e;
   const int blocks = (152 * 8 + p.B * p.H - 1) / (p.B * p.H);
-  evict_move_kernel<<<p.B * p.H * blocks, kMoveThreads, 0, stream>>>(p, blocks);
-  return cudaGetLastError();
+  return ds::launch_after(evict_move_kernel, static_cast<unsigned>(p.B * p.H * blocks), kMoveThreads, 0, stream, p, blocks);
 }
 
 }  // namespace spa

@@ -261,6 +261,7 @@ struct EvictParams {
   int* ws;                  // per (b, h): move count, then (destination, source) pairs
   int B, H, m, dv, cap, budget, sink, recent;
 };
+constexpr int kEvictMaxRows = 1 << 20;  // a bit of shared memory per row
 // ints of workspace per (b, h)
 __host__ __device__ inline size_t evict_stride(int cap, int budget) {
   const long long moves = cap - budget < budget ? cap - budget : budget;

@@ -1252,6 +1252,7 @@ int spa_kcache_evict(void* kc, float* kc_mul, void* v, const float* acc, const i
   if (st) return st;
   if (need == 0) return SPA_OK;
   if (sink < 0 || recent < 0 || static_cast<long long>(sink) + recent > budget) return SPA_ERR_SHAPE;
+  if (cap > spa::kEvictMaxRows) return SPA_ERR_UNSUPPORTED;
   if ((m != 16 && m != 32 && m != 64 && m != 128) || (d_v != 64 && d_v != 128))
     return SPA_ERR_UNSUPPORTED;
   if (!kc || !kc_mul || !v || !acc || !row_pos || !lens || !acc_out || !row_pos_out || !lens_out ||

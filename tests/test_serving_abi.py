@@ -142,6 +142,7 @@ def test_evict_rejects_bad_arguments(lib):
     assert evict(lib, sink=13, recent=4) == SHAPE
     assert evict(lib, B=300, H=300) == SHAPE
     assert evict(lib, m=33) == UNSUPPORTED
+    assert evict(lib, cap=2**20 + 1) == UNSUPPORTED
     assert evict(lib, dv=65) == UNSUPPORTED
     assert evict(lib, size=16) == NOMEM
     assert evict(lib, ws=A + 16) == ALIGN

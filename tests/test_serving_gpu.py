@@ -493,7 +493,11 @@ EVICT = [
     (1, 2, 32, 64, 5000, 4999, 10, 4000, [5000]),
     (1, 1, 32, 64, 20000, 64, 0, 64, [20000]),
     (2, 1, 16, 64, 100, 100, 50, 50, [100, 2**31 - 1]),
-    (1, 1, 32, 128, 70000, 30000, 4, 512, [70000]),
+    (1, 1, 32, 128, 70000, 30000, 4, 512, [70000]),           # keys that do not fit in shared memory
+    (61, 5, 16, 64, 70, 33, 1, 8, [(i * 7) % 71 for i in range(61)]),
+    (2, 3, 16, 64, 9000, 4000, 3, 64, [9000, 8191]),
+    (2, 1, 16, 64, 30000, 29000, 3, 64, [30000, 29001]),      # keys in shared memory
+    (1, 2, 16, 64, 8192, 8191, 3, 64, [8192]),
 ]
 
 
