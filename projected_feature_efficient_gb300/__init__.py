@@ -30,5 +30,7 @@ __all__ = [
 
 def __getattr__(name):
     if name in __all__:
-        return getattr(importlib.import_module("._binding", __name__), name)
+        value = getattr(importlib.import_module("._binding", __name__), name)
+        globals()[name] = value  # later uses find it without this function
+        return value
     raise AttributeError(name)

@@ -5,6 +5,7 @@ functions raise ``SpaError`` on any non-zero status.  Names follow the C ABI.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -377,35 +378,22 @@ def spa_attention_decode(q, P, kc, kc_mul, v, L, out=None, stream=None):
 SPA_ROPE_PLAIN, SPA_ROPE_LINEAR, SPA_ROPE_BASE, SPA_ROPE_RAMP = 0, 1, 2, 3
 
 
-class _On:
-    """The device and stream of a call: the arguments' device is made current
-    for its duration, and `stream` (default: the device's current one) is the
-    stream of its launches and of the tensors it allocates."""
+_here = contextlib.nullcontext()
 
-    __slots__ = ("index", "raw", "_guards")
 
-    def __init__(self, device, stream):
-        import torch
-        self.index = device.index
-        self._guards = ()
-        if stream is not None:
-            if stream.device_index != device.index:
-                raise ValueError("the stream belongs to another device than the tensors")
-            self._guards = (torch.cuda.stream(stream),)
-            self.raw = stream.cuda_stream
-        else:
-            if torch.cuda.current_device() != device.index:
-                self._guards = (torch.cuda.device(device.index),)
-            self.raw = torch._C._cuda_getCurrentRawStream(device.index)
-
-    def __enter__(self):
-        for g in self._guards:
-            g.__enter__()
-        return self
-
-    def __exit__(self, *exc):
-        for g in reversed(self._guards):
-            g.__exit__(*exc)
+def _on(device, stream):
+    """The raw stream of a call and the context for it: the arguments' device is
+    current, and `stream` (default: the device's current one) is the stream of
+    the call's launches and of the tensors it allocates."""
+    import torch
+    if stream is not None:
+        if stream.device_index != device.index:
+            raise ValueError("the stream belongs to another device than the tensors")
+        return stream.cuda_stream, torch.cuda.stream(stream)
+    raw = torch._C._cuda_getCurrentRawStream(device.index)
+    if torch._C._cuda_getDevice() != device.index:
+        return raw, torch.cuda.device(device.index)
+    return raw, _here
 
 
 def _device_of(t):
@@ -416,15 +404,15 @@ def _device_of(t):
 
 def _arg(name, t, shape, dtype, device):
     """A dense tensor of this shape, type and device; its address."""
+    if t.shape == shape and t.dtype is dtype and t.device == device and t.is_contiguous():
+        return t.data_ptr()
     if t.shape != shape:
         raise ValueError(f"{name} must have the shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.device != device:
         raise ValueError(f"{name} must be on {device}, got {t.device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _workspace(t, device):
@@ -490,7 +478,8 @@ def spa_rope(q, table, pos=None, *, k=None, rot=None, interleaved=False, inverse
             raise ValueError(f"k must be on {device}, got {k.device}")
     elif k_out is not None:
         raise ValueError("k_out without k")
-    with _On(device, stream) as on:
+    raw, context = _on(device, stream)
+    with context:
         if out is None:
             out = torch.empty((B, H, N, d), dtype=q.dtype, device=device)
         if k is not None and k_out is None:
@@ -507,7 +496,7 @@ def spa_rope(q, table, pos=None, *, k=None, rot=None, interleaved=False, inverse
         strides = _Strides(a[0], a[1], a[2], b[0], b[1], b[2], c[0], c[1], c[2], e[0], e[1], e[2])
         _check(lib.spa_rope(q.data_ptr(), k.data_ptr() if Hk else None, out.data_ptr(),
                             k_out.data_ptr() if Hk else None, strides, ppos, pos0, ptable, B, H, Hk,
-                            N, d, rot, bool(interleaved), bool(inverse), scale, code, on.raw),
+                            N, d, rot, bool(interleaved), bool(inverse), scale, code, raw),
                "spa_rope")
     return out if k is None else (out, k_out)
 
@@ -533,8 +522,9 @@ def spa_kcache_append_ragged(k, v, P, kc, kc_mul, vc, pos, count=None, acc=None,
             None if acc is None else _arg("acc", acc, row, f32, device),
             None if row_pos is None else _arg("row_pos", row_pos, row, i32, device),
             None if token is None else _arg("token", token, (B,), i32, device))
-    with _On(device, stream) as on:
-        _check(lib.spa_kcache_append_ragged(*args, B, H, T, d, m, dv, cap, SPA_BF16, on.raw),
+    raw, context = _on(device, stream)
+    with context:
+        _check(lib.spa_kcache_append_ragged(*args, B, H, T, d, m, dv, cap, SPA_BF16, raw),
                "spa_kcache_append_ragged")
 
 
@@ -577,13 +567,14 @@ def spa_attention_decode_shared(q, P, kc, kc_mul, v, lens, *, prefix=None, plen=
         acc_out = acc
     weights = (None if acc is None else _arg("acc", acc, (B, Hk, cap), f32, device),
                None if acc_out is None else _arg("acc_out", acc_out, (B, Hk, cap), f32, device))
-    with _On(device, stream) as on:
+    raw, context = _on(device, stream)
+    with context:
         if out is None:
             out = torch.empty((B, H, dv), dtype=bf16, device=device)
         pout = _arg("out", out, (B, H, dv), bf16, device)
         ws, size = _workspace(workspace, device)
         _check(lib.spa_attention_decode_shared(*own, *shared, pout, *weights, B, H, Hk, plen, pcap,
-                                               d, m, dv, cap, SPA_BF16, ws, size, on.raw),
+                                               d, m, dv, cap, SPA_BF16, ws, size, raw),
                "spa_attention_decode_shared")
     return out
 
@@ -618,13 +609,14 @@ def spa_kcache_evict(kc, kc_mul, v, acc, row_pos, lens, budget, sink=0, recent=0
             _arg("lens", lens, (B,), i32, device), _arg("acc_out", acc_out, row, f32, device),
             _arg("row_pos_out", row_pos_out, row, i32, device),
             _arg("lens_out", lens_out, (B,), i32, device))
-    with _On(device, stream) as on:
+    raw, context = _on(device, stream)
+    with context:
         if src is None:
             src = torch.empty((B, H, max(budget, 0)), dtype=i32, device=device)
         psrc = _arg("src", src, (B, H, max(budget, 0)), i32, device)
         ws, size = _workspace(workspace, device)
         _check(lib.spa_kcache_evict(*args, psrc, B, H, m, dv, cap, budget, int(sink), int(recent),
-                                    ws, size, on.raw), "spa_kcache_evict")
+                                    ws, size, raw), "spa_kcache_evict")
     return src
 
 

@@ -605,8 +605,8 @@ __global__ void __launch_bounds__(kCombineThreads)
 template <int M, int DV>
 cudaError_t launch_own_t(const Params& a, const Maps& maps, cudaStream_t stream) {
   using P = OwnPlan<M, DV>;
-  const cudaError_t e = cudaFuncSetAttribute(decode_own_kernel<M, DV>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             P::kBytes);
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = allow_smem(decode_own_kernel<M, DV>, P::kBytes, done);
   if (e != cudaSuccess) return e;
   return launch_after(decode_own_kernel<M, DV>, a.g.workers / kOwnWarps, 32 * kOwnWarps, P::kBytes, stream, a, maps);
 }

@@ -850,8 +850,8 @@ size_t layout(const DecodeSharedParams& p, const Geo& g, char* ws, Work* w) {
 template <int M, int DV>
 cudaError_t launch(const Params& a, const Maps& maps, cudaStream_t stream) {
   using P = Plan<M, DV>;
-  const cudaError_t e = cudaFuncSetAttribute(decode_prefix_kernel<M, DV>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, P::kLaunch);
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = allow_smem(decode_prefix_kernel<M, DV>, P::kLaunch, done);
   if (e != cudaSuccess) return e;
   return launch_after(decode_prefix_kernel<M, DV>, a.g.grid, kThreads, P::kLaunch, stream, a, maps);
 }

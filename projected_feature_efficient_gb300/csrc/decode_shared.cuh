@@ -13,6 +13,7 @@
 // Every part of a row's keys leaves unnormalised sums, a maximum and a sum of
 // probabilities in the workspace.
 #pragma once
+#include <atomic>
 #include <cstdint>
 
 #include "kernels.cuh"
@@ -151,6 +152,19 @@ __device__ __forceinline__ float warp_sum(float v) {
 // starts; its results are there after the wait.
 __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+// A kernel's dynamic shared memory, set once per device (every launch sets the same).
+template <class Kernel>
+cudaError_t allow_smem(Kernel kernel, int bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (dev < 64 && (done.load(std::memory_order_relaxed) & bit)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && dev < 64) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
 
 template <class... P, class... A>
 cudaError_t launch_after(void (*kernel)(P...), unsigned grid, unsigned block, size_t smem, cudaStream_t stream,
