@@ -57,15 +57,31 @@ template <int M>
 __device__ __forceinline__ void stage_projection(uint2* frag, const __nv_bfloat16* P, int d,
                                                  int groups, int tid) {
   uint16_t* f = reinterpret_cast<uint16_t*>(frag);
-  for (int i = tid; i < groups * 32 * M; i += kThreads) {
-    const int k = i / M, n = i % M;
-    const uint16_t w = k < d ? __bfloat16_as_ushort(P[i]) : uint16_t(0);
-    const int g = k >> 5, q = (k >> 3) & 3, r = k & 7;
-    const int step = 2 * g + (r >> 2), pos = r & 3;  // pos 0,1: first register, 2,3: second
-    // column n = qn*(M/4) + 2j + o is fragment column 2*qn + o of tile j
-    const int qn = n / (M / 4), j = (n % (M / 4)) >> 1, o = n & 1;
-    const int lane = (2 * qn + o) * 4 + q;  // B fragment: lane = column * 4 + quarter
-    f[((step * (M / 8) + j) * 32 + lane) * 4 + pos] = w;
+  const int vectors = groups * 32 * (M / 8);  // 8 columns of one feature each
+  constexpr int E = 8;                        // loads in flight
+  for (int i0 = tid; i0 < vectors; i0 += E * kThreads) {
+    uint4 x[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const int i = i0 + e * kThreads, k = i / (M / 8);
+      x[e] = i < vectors && k < d ? __ldg(reinterpret_cast<const uint4*>(P) + i) : make_uint4(0u, 0u, 0u, 0u);
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const int i = i0 + e * kThreads;
+      if (i >= vectors) break;
+      const int k = i / (M / 8), n0 = 8 * (i % (M / 8));
+      const int g = k >> 5, q = (k >> 3) & 3, r = k & 7;
+      const int step = 2 * g + (r >> 2), pos = r & 3;  // pos 0,1: first register, 2,3: second
+      const uint32_t w[4] = {x[e].x, x[e].y, x[e].z, x[e].w};
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        // column n = qn*(M/4) + 2j + o is fragment column 2*qn + o of tile j
+        const int n = n0 + u, qn = n / (M / 4), j = (n % (M / 4)) >> 1, o = n & 1;
+        const int lane = (2 * qn + o) * 4 + q;  // B fragment: lane = column * 4 + quarter
+        f[((step * (M / 8) + j) * 32 + lane) * 4 + pos] = static_cast<uint16_t>(w[u >> 1] >> (16 * (u & 1)));
+      }
+    }
   }
 }
 
@@ -80,20 +96,51 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p, 
   __syncthreads();
   const long long R = static_cast<long long>(p.B) * p.T;
   const bool wide = p.d % 8 == 0;
+  // Value rows: lanes take the tile's rows two (four) at a time, a piece of 16 bytes
+  // each; where a row comes from and goes to is known to the lanes that have it.
+  constexpr int kPieces = 4;
+  const int pieces = p.dv / 8;  // per row: 8 or 16
+  auto piece_of = [&](int i, int* row) {
+    const int at = 32 * i + lane;
+    *row = at / pieces;
+    return at - *row * pieces;
+  };
+  auto row_of = [&](const long long (&x)[2], int row) {
+    const long long a = __shfl_sync(0xffffffffu, x[0], (row & 7) * 4), b = __shfl_sync(0xffffffffu, x[1], (row & 7) * 4);
+    return row < 8 ? a : b;
+  };
+  auto load_values = [&](const long long (&from)[2], const long long (&dst)[2], int i0, uint4 (&v)[kPieces]) {
+#pragma unroll
+    for (int e = 0; e < kPieces; ++e) {
+      int row;
+      const int piece = piece_of(i0 + e, &row);
+      const long long s = row_of(from, row), t = row_of(dst, row);
+      if (t >= 0) v[e] = __ldg(reinterpret_cast<const uint4*>(p.v + s * p.dv) + piece);
+    }
+  };
+  auto store_values = [&](const long long (&dst)[2], int i0, const uint4 (&v)[kPieces]) {
+#pragma unroll
+    for (int e = 0; e < kPieces; ++e) {
+      int row;
+      const int piece = piece_of(i0 + e, &row);
+      const long long t = row_of(dst, row);
+      if (t >= 0) *(reinterpret_cast<uint4*>(p.vc + t * p.dv) + piece) = v[e];
+    }
+  };
   for (int tile = blockIdx.x * kWarps + warp; tile < tiles; tile += gridDim.x * kWarps) {
-    // this lane's two rows: where they come from and where they go (-1: nowhere)
-    const __nv_bfloat16* x[2];
-    long long dst[2];
+    // this lane's two rows: where they come from (a row of k and v) and where they go
+    // (-1: nowhere)
+    long long from[2], dst[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const long long r = static_cast<long long>(tile) * 16 + r0 + 8 * i;
-      x[i] = nullptr;
+      from[i] = 0;
       dst[i] = -1;
       if (r < R) {
         const int b = static_cast<int>(r / p.T), t = static_cast<int>(r - static_cast<long long>(b) * p.T);
         const long long at = static_cast<long long>(p.pos[b]) + t;
         if ((!p.count || t < p.count[b]) && at >= 0 && at < p.cap) {
-          x[i] = p.k + (static_cast<size_t>(b) * p.H + h) * p.T * p.d + static_cast<size_t>(t) * p.d;
+          from[i] = (static_cast<long long>(b) * p.H + h) * p.T + t;
           dst[i] = (static_cast<long long>(b) * p.H + h) * p.cap + at;
           if (q == 0) {
             if (p.acc) p.acc[dst[i]] = 0.f;
@@ -102,37 +149,51 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p, 
         }
       }
     }
+    if (!__any_sync(0xffffffffu, dst[0] >= 0 || dst[1] >= 0)) continue;
+    const __nv_bfloat16* x[2] = {p.k + from[0] * p.d, p.k + from[1] * p.d};
     float c[M / 8][4];
 #pragma unroll
     for (int j = 0; j < M / 8; ++j)
 #pragma unroll
       for (int e = 0; e < 4; ++e) c[j][e] = 0.f;
-    for (int g = 0; g < groups; ++g) {
-      uint32_t w[2][4];
-      const int k = 32 * g + 8 * q;
+    uint4 vp[kPieces];  // the value rows' first pieces, in flight with the keys
+    load_values(from, dst, 0, vp);
+    for (int g0 = 0; g0 < groups; g0 += 4) {  // 128 features in flight
+      uint4 w[4][2];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        if (x[i] && wide && k < p.d) {
-          const uint4 v = __ldg(reinterpret_cast<const uint4*>(x[i] + k));
-          w[i][0] = v.x; w[i][1] = v.y; w[i][2] = v.z; w[i][3] = v.w;
-        } else if (x[i] && !wide) {
+      for (int g = 0; g < 4; ++g) {
+        const int k = 32 * (g0 + g) + 8 * q;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) w[i][e] = pair_at(x[i], k + 2 * e, p.d);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) w[i][e] = 0u;
+        for (int i = 0; i < 2; ++i) {
+          w[g][i] = make_uint4(0u, 0u, 0u, 0u);
+          if (dst[i] < 0 || k >= p.d) continue;
+          if (wide) {
+            w[g][i] = __ldg(reinterpret_cast<const uint4*>(x[i] + k));
+          } else {
+            w[g][i] = make_uint4(pair_at(x[i], k, p.d), pair_at(x[i], k + 2, p.d), pair_at(x[i], k + 4, p.d),
+                                 pair_at(x[i], k + 6, p.d));
+          }
         }
       }
 #pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        const uint32_t a[4] = {w[0][2 * s], w[1][2 * s], w[0][2 * s + 1], w[1][2 * s + 1]};
-        const uint2* f = frag + ((2 * g + s) * (M / 8)) * 32 + lane;
+      for (int g = 0; g < 4; ++g) {
+        if (g0 + g >= groups) break;
 #pragma unroll
-        for (int j = 0; j < M / 8; ++j) {
-          const uint2 b = f[j * 32];
-          mma_bf16(c[j], a, b.x, b.y);
+        for (int s = 0; s < 2; ++s) {
+          const uint32_t a[4] = {s ? w[g][0].z : w[g][0].x, s ? w[g][1].z : w[g][1].x,
+                                 s ? w[g][0].w : w[g][0].y, s ? w[g][1].w : w[g][1].y};
+          const uint2* f = frag + ((2 * (g0 + g) + s) * (M / 8)) * 32 + lane;
+#pragma unroll
+          for (int j = 0; j < M / 8; ++j) {
+            const uint2 b = f[j * 32];
+            mma_bf16(c[j], a, b.x, b.y);
+          }
         }
       }
+    }
+    for (int i = 0; i < pieces / 2; i += kPieces) {  // the value rows, 16 bytes per lane
+      if (i > 0) load_values(from, dst, i, vp);
+      store_values(dst, i, vp);
     }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -180,19 +241,6 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p, 
           *reinterpret_cast<uint4*>(o + 2 * j) = make_uint4(hw[j], hw[j + 1], hw[j + 2], hw[j + 3]);
       }
       if (q == 0) p.kc_mul[dst[i]] = pow2i(e);
-    }
-    // the value rows of the tile, 16 bytes per lane
-    const int pieces = p.dv / 8;
-    for (int i = lane; i < 16 * pieces; i += 32) {
-      const int row = i / pieces, piece = i % pieces;
-      const long long r = static_cast<long long>(tile) * 16 + row;
-      if (r >= R) break;
-      const int b = static_cast<int>(r / p.T), t = static_cast<int>(r - static_cast<long long>(b) * p.T);
-      const long long at = static_cast<long long>(p.pos[b]) + t;
-      if ((p.count && t >= p.count[b]) || at < 0 || at >= p.cap) continue;
-      const size_t from = ((static_cast<size_t>(b) * p.H + h) * p.T + t) * p.dv + piece * 8;
-      const size_t to = ((static_cast<size_t>(b) * p.H + h) * p.cap + at) * p.dv + piece * 8;
-      *reinterpret_cast<uint4*>(p.vc + to) = __ldg(reinterpret_cast<const uint4*>(p.v + from));
     }
   }
 }

@@ -76,49 +76,67 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeParams p, int 
   const int half = p.rot / 2;
   // first element of the unit; the tail of the half layout starts at rot
   const int e0 = INTER ? u * V : turns ? u * V : p.rot + (u - turning) * V;
-  for (int h = h0; h < h1; ++h) {
+  using W = Vec<T, V>;
+  constexpr int E = 4;  // heads in flight
+  constexpr bool kTwo = !INTER;  // a vector of each half
+  auto place = [&](int h, const T*& x, T*& y) {
     const int t = h < p.H[0] ? 0 : 1;
     const int hh = t ? h - p.H[0] : h;
-    const T* x = static_cast<const T*>(p.x[t]) + b * p.xs[t][0] + hh * p.xs[t][1] + n * p.xs[t][2] + e0;
-    T* y = static_cast<T*>(p.y[t]) + b * p.ys[t][0] + hh * p.ys[t][1] + n * p.ys[t][2] + e0;
-    using W = Vec<T, V>;
-    if (!turns && LOOSE) {
-      y[0] = x[0];
-      if (e0 + 1 < p.d) y[1] = x[1];
-    } else if (!turns) {
-      *reinterpret_cast<W*>(y) = *reinterpret_cast<const W*>(x);
-    } else if constexpr (INTER) {
-      W w;
-      if constexpr (LOOSE) {
-        w.e[0] = x[0];
-        w.e[1] = e0 + 1 < p.d ? x[1] : x[0];
-      } else {
-        w = *reinterpret_cast<const W*>(x);
-      }
+    x = static_cast<const T*>(p.x[t]) + b * p.xs[t][0] + hh * p.xs[t][1] + n * p.xs[t][2] + e0;
+    y = static_cast<T*>(p.y[t]) + b * p.ys[t][0] + hh * p.ys[t][1] + n * p.ys[t][2] + e0;
+  };
+  for (int hb = h0; hb < h1; hb += E) {
+    W wa[E], wb[kTwo ? E : 1];
 #pragma unroll
-      for (int i = 0; i < V / 2; ++i) {
-        if (u * (V / 2) + i < half) {  // a vector may end in the tail: those features stay as they are
-          const float a = up(w.e[2 * i]), bb = up(w.e[2 * i + 1]);
-          down(w.e[2 * i], a * c[i] - bb * s[i]);
-          down(w.e[2 * i + 1], a * s[i] + bb * c[i]);
+    for (int e = 0; e < E; ++e) {
+      if (hb + e >= h1) break;
+      const T* x;
+      T* y;
+      place(hb + e, x, y);
+      if constexpr (LOOSE) {
+        wa[e].e[0] = x[0];
+        wa[e].e[1] = e0 + 1 < p.d ? x[1] : x[0];
+      } else {
+        wa[e] = *reinterpret_cast<const W*>(x);
+        if constexpr (kTwo)
+          if (turns) wb[e] = *reinterpret_cast<const W*>(x + half);
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      if (hb + e >= h1) break;
+      const T* x;
+      T* y;
+      place(hb + e, x, y);
+      if constexpr (INTER) {
+        if (turns) {
+#pragma unroll
+          for (int i = 0; i < V / 2; ++i) {
+            if (u * (V / 2) + i < half) {  // a vector may end in the tail: those features stay as they are
+              const float a = up(wa[e].e[2 * i]), bb = up(wa[e].e[2 * i + 1]);
+              down(wa[e].e[2 * i], a * c[i] - bb * s[i]);
+              down(wa[e].e[2 * i + 1], a * s[i] + bb * c[i]);
+            }
+          }
         }
-      }
-      if constexpr (LOOSE) {
-        y[0] = w.e[0];
-        if (e0 + 1 < p.d) y[1] = w.e[1];
+        if constexpr (LOOSE) {
+          y[0] = wa[e].e[0];
+          if (e0 + 1 < p.d) y[1] = wa[e].e[1];
+        } else {
+          *reinterpret_cast<W*>(y) = wa[e];
+        }
       } else {
-        *reinterpret_cast<W*>(y) = w;
-      }
-    } else {
-      W wa = *reinterpret_cast<const W*>(x), wb = *reinterpret_cast<const W*>(x + half);
+        if (turns) {
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const float a = up(wa.e[i]), bb = up(wb.e[i]);
-        down(wa.e[i], a * c[i] - bb * s[i]);
-        down(wb.e[i], a * s[i] + bb * c[i]);
+          for (int i = 0; i < V; ++i) {
+            const float a = up(wa[e].e[i]), bb = up(wb[e].e[i]);
+            down(wa[e].e[i], a * c[i] - bb * s[i]);
+            down(wb[e].e[i], a * s[i] + bb * c[i]);
+          }
+          *reinterpret_cast<W*>(y + half) = wb[e];
+        }
+        *reinterpret_cast<W*>(y) = wa[e];
       }
-      *reinterpret_cast<W*>(y) = wa;
-      *reinterpret_cast<W*>(y + half) = wb;
     }
   }
 }
