@@ -27,10 +27,20 @@ struct alignas(sizeof(T) * V) Vec {
   T e[V];
 };
 
+// Two neighbouring elements of a vector at a time: one conversion of a bf16 pair.
+template <int V>
+__device__ __forceinline__ void put2(Vec<float, V>& w, int i, float x, float y) {
+  w.e[i] = x;
+  if (V > 1) w.e[V > 1 ? i + 1 : i] = y;
+}
+template <int V>
+__device__ __forceinline__ void put2(Vec<__nv_bfloat16, V>& w, int i, float x, float y) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(x, y);
+  w.e[i] = v.x;
+  if (V > 1) w.e[V > 1 ? i + 1 : i] = v.y;
+}
 __device__ __forceinline__ float up(float x) { return x; }
 __device__ __forceinline__ float up(__nv_bfloat16 x) { return __bfloat162float(x); }
-__device__ __forceinline__ void down(float& y, float x) { y = x; }
-__device__ __forceinline__ void down(__nv_bfloat16& y, float x) { y = __float2bfloat16_rn(x); }
 
 __device__ __forceinline__ void sincos_of(const RopeParams& p, int pair, int pos, float& s,
                                           float& c) {
@@ -79,64 +89,66 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeParams p, int 
   using W = Vec<T, V>;
   constexpr int E = 4;  // heads in flight
   constexpr bool kTwo = !INTER;  // a vector of each half
-  auto place = [&](int h, const T*& x, T*& y) {
-    const int t = h < p.H[0] ? 0 : 1;
-    const int hh = t ? h - p.H[0] : h;
-    x = static_cast<const T*>(p.x[t]) + b * p.xs[t][0] + hh * p.xs[t][1] + n * p.xs[t][2] + e0;
-    y = static_cast<T*>(p.y[t]) + b * p.ys[t][0] + hh * p.ys[t][1] + n * p.ys[t][2] + e0;
-  };
-  for (int hb = h0; hb < h1; hb += E) {
-    W wa[E], wb[kTwo ? E : 1];
+  auto turn = [&](W& wa, W& wb) {
+    if constexpr (INTER) {
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      if (hb + e >= h1) break;
-      const T* x;
-      T* y;
-      place(hb + e, x, y);
-      if constexpr (LOOSE) {
-        wa[e].e[0] = x[0];
-        wa[e].e[1] = e0 + 1 < p.d ? x[1] : x[0];
-      } else {
-        wa[e] = *reinterpret_cast<const W*>(x);
-        if constexpr (kTwo)
-          if (turns) wb[e] = *reinterpret_cast<const W*>(x + half);
+      for (int i = 0; i < V / 2; ++i) {
+        if (u * (V / 2) + i < half) {  // a vector may end in the tail: those features stay as they are
+          const float a = up(wa.e[2 * i]), bb = up(wa.e[2 * i + 1]);
+          put2(wa, 2 * i, a * c[i] - bb * s[i], a * s[i] + bb * c[i]);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; i += 2) {
+        const int k = V > 1 ? i + 1 : i;
+        const float a0 = up(wa.e[i]), b0 = up(wb.e[i]), a1 = up(wa.e[k]), b1 = up(wb.e[k]);
+        put2(wa, i, a0 * c[i] - b0 * s[i], a1 * c[k] - b1 * s[k]);
+        put2(wb, i, a0 * s[i] + b0 * c[i], a1 * s[k] + b1 * c[k]);
       }
     }
+  };
+  auto read = [&](const T* x, W& wa, W& wb) {
+    if constexpr (LOOSE) {
+      wa.e[0] = x[0];
+      wa.e[1] = e0 + 1 < p.d ? x[1] : x[0];
+    } else {
+      wa = *reinterpret_cast<const W*>(x);
+      if (kTwo && turns) wb = *reinterpret_cast<const W*>(x + half);
+    }
+  };
+  auto write = [&](T* y, const W& wa, const W& wb) {
+    if constexpr (LOOSE) {
+      y[0] = wa.e[0];
+      if (e0 + 1 < p.d) y[1] = wa.e[1];
+    } else {
+      *reinterpret_cast<W*>(y) = wa;
+      if (kTwo && turns) *reinterpret_cast<W*>(y + half) = wb;
+    }
+  };
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      if (hb + e >= h1) break;
-      const T* x;
-      T* y;
-      place(hb + e, x, y);
-      if constexpr (INTER) {
-        if (turns) {
+  for (int t = 0; t < 2; ++t) {  // heads h0 .. h1-1 of the two tensors' one after the other
+    const int from = max(h0 - (t ? p.H[0] : 0), 0), to = min(h1 - (t ? p.H[0] : 0), p.H[t]);
+    if (from >= to) continue;
+    const long long xs = p.xs[t][1], ys = p.ys[t][1];
+    const T* x = static_cast<const T*>(p.x[t]) + b * p.xs[t][0] + n * p.xs[t][2] + from * xs + e0;
+    T* y = static_cast<T*>(p.y[t]) + b * p.ys[t][0] + n * p.ys[t][2] + from * ys + e0;
+    int left = to - from;
+    for (; left >= E; left -= E, x += E * xs, y += E * ys) {
+      W wa[E], wb[E];
 #pragma unroll
-          for (int i = 0; i < V / 2; ++i) {
-            if (u * (V / 2) + i < half) {  // a vector may end in the tail: those features stay as they are
-              const float a = up(wa[e].e[2 * i]), bb = up(wa[e].e[2 * i + 1]);
-              down(wa[e].e[2 * i], a * c[i] - bb * s[i]);
-              down(wa[e].e[2 * i + 1], a * s[i] + bb * c[i]);
-            }
-          }
-        }
-        if constexpr (LOOSE) {
-          y[0] = wa[e].e[0];
-          if (e0 + 1 < p.d) y[1] = wa[e].e[1];
-        } else {
-          *reinterpret_cast<W*>(y) = wa[e];
-        }
-      } else {
-        if (turns) {
+      for (int e = 0; e < E; ++e) read(x + e * xs, wa[e], wb[e]);
 #pragma unroll
-          for (int i = 0; i < V; ++i) {
-            const float a = up(wa[e].e[i]), bb = up(wb[e].e[i]);
-            down(wa[e].e[i], a * c[i] - bb * s[i]);
-            down(wb[e].e[i], a * s[i] + bb * c[i]);
-          }
-          *reinterpret_cast<W*>(y + half) = wb[e];
-        }
-        *reinterpret_cast<W*>(y) = wa[e];
+      for (int e = 0; e < E; ++e) {
+        if (turns) turn(wa[e], wb[e]);
+        write(y + e * ys, wa[e], wb[e]);
       }
+    }
+    for (; left > 0; --left, x += xs, y += ys) {
+      W wa, wb;
+      read(x, wa, wb);
+      if (turns) turn(wa, wb);
+      write(y, wa, wb);
     }
   }
 }
