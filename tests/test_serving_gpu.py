@@ -349,6 +349,11 @@ DECODE = [
     (24, 16, 8, 64, 64, 128, 700, 9000, [(97 * i) % 701 for i in range(24)]),
     (40, 48, 4, 64, 16, 64, 520, 4000, [(131 * i) % 521 for i in range(40)]),   # and several row tiles
     (3, 8, 4, 64, 128, 128, 4000, 20000, [4000, 1, 129]),                       # a ring of two slots
+    # many short sequences, without and with a prefix, and few warps' work for many
+    (1300, 2, 1, 64, 16, 64, 40, 0, [(7 * i) % 41 for i in range(1300)]),
+    (1100, 2, 2, 64, 32, 64, 24, 300, [(5 * i) % 25 for i in range(1100)]),
+    (70, 4, 4, 64, 16, 64, 2000, 0, [0] * 69 + [2000]),
+    (70, 4, 4, 64, 32, 64, 2000, 6000, [2000] + [0] * 69),
 ]
 
 
