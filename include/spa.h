@@ -532,6 +532,21 @@ SPA_API int spa_selftest_proj_wait_timeout(int limit_ms, int m);
 SPA_API int spa_selftest_copy_wait_timeout(int limit_ms, int kernel);
 
 /*
+ * spa_selftest_decode_wait_timeout -- the same self-test for the kernels of
+ * spa_attention_decode_shared: kernel 0 the prefix kernel, 1 the kernel of the
+ * sequences' own rows, each alone in a small call (B=2 H=4 Hk=1 d=64 m=32
+ * d_v=64, 1024 rows, zero inputs, buffers taken and released with
+ * cudaMalloc/cudaFree).  In kernel 0 every CTA withholds its first "scores
+ * ready" arrival, in kernel 1 the first warp leaves its first copies unissued.
+ * Every wait is limited to limit_ms (1..2000).  Returns SPA_ERR_TIMEOUT when
+ * the kernel reported the timeout (the expected outcome), SPA_OK when it did
+ * not, SPA_ERR_SHAPE for limit_ms out of range, SPA_ERR_UNSUPPORTED for another
+ * kernel number, or another status if a call failed.  The device stays usable
+ * afterwards.
+ */
+SPA_API int spa_selftest_decode_wait_timeout(int limit_ms, int kernel);
+
+/*
  * spa_device_error -- reads and clears the device error word of the current
  * device (synchronising it first).  *code receives 0 when no kernel gave up
  * on a bounded wait since the last call, else SPA_ERR_TIMEOUT.

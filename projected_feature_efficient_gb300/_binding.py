@@ -53,6 +53,8 @@ lib.spa_selftest_proj_wait_timeout.argtypes = [_i, _i]
 lib.spa_selftest_proj_wait_timeout.restype = _i
 lib.spa_selftest_copy_wait_timeout.argtypes = [_i, _i]
 lib.spa_selftest_copy_wait_timeout.restype = _i
+lib.spa_selftest_decode_wait_timeout.argtypes = [_i, _i]
+lib.spa_selftest_decode_wait_timeout.restype = _i
 lib.spa_attention_bwd.argtypes = [_vp] * 10 + [_i] * 8 + [_vp]
 lib.spa_attention_bwd.restype = _i
 lib.spa_host_pool_trim.argtypes = []
@@ -642,6 +644,12 @@ def selftest_copy_wait_timeout(limit_ms: int = 50, kernel: int = 0) -> int:
     (kernel 0: the backward's statistics, 1: its finish, 2: the Top-k);
     returns the status code."""
     return int(lib.spa_selftest_copy_wait_timeout(int(limit_ms), int(kernel)))
+
+
+def selftest_decode_wait_timeout(limit_ms: int = 50, kernel: int = 0) -> int:
+    """The same self-test for the shared-prefix decode (kernel 0: the prefix
+    kernel, 1: the kernel of the sequences' own rows); returns the status code."""
+    return int(lib.spa_selftest_decode_wait_timeout(int(limit_ms), int(kernel)))
 
 
 def device_error() -> int:

@@ -1592,6 +1592,52 @@ int spa_selftest_bwd_wait_timeout(int limit_ms) {
   return word ? SPA_ERR_TIMEOUT : SPA_OK;
 }
 
+int spa_selftest_decode_wait_timeout(int limit_ms, int kernel) {
+  if (limit_ms <= 0 || limit_ms > 2000) return SPA_ERR_SHAPE;
+  if (kernel < 0 || kernel > 1) return SPA_ERR_UNSUPPORTED;
+  // two sequences, four query heads on one key head; the prefix kernel alone or
+  // the kernel of the sequences' own rows alone
+  constexpr int B = 2, H = 4, Hk = 1, d = 64, m = 32, dv = 64, rows = 1024;
+  const int plen = kernel == 0 ? rows : 0, cap = kernel == 1 ? rows : 0;
+  spa::DecodeSharedParams dp{};
+  int st = decode_shared_sizes(dp, B, H, Hk, plen, d, m, dv, cap);
+  if (st) return st;
+  const size_t nq = static_cast<size_t>(B) * H * d * 2, np = static_cast<size_t>(Hk) * d * m * 2;
+  const size_t nk = static_cast<size_t>(B) * Hk * rows * m * 2, ne = static_cast<size_t>(B) * Hk * rows * 4;
+  const size_t nv = static_cast<size_t>(B) * Hk * rows * dv * 2, no = static_cast<size_t>(B) * H * dv * 2;
+  const size_t oq = 0, op = align256(oq + nq), ok = align256(op + np), oe = align256(ok + nk),
+               ov = align256(oe + ne), ol = align256(ov + nv), oo = align256(ol + B * sizeof(int)),
+               ow = align256(oo + no);
+  const size_t total = ow + spa::decode_shared_workspace(dp);
+  int* err = nullptr;
+  if ((st = device_error_ptr(&err))) return st;
+  char* buf = nullptr;
+  if (cudaMalloc(reinterpret_cast<void**>(&buf), total) != cudaSuccess) {
+    cudaGetLastError();
+    return SPA_ERR_NOMEM;
+  }
+  st = cuda_status(cudaMemset(buf, 0, total));  // zero inputs
+  if (!st) st = cuda_status(cudaMemset(buf + ol, 1, B * sizeof(int)));  // lengths beyond the capacity: all rows
+  dp.q = reinterpret_cast<const __nv_bfloat16*>(buf + oq);
+  dp.P = reinterpret_cast<const __nv_bfloat16*>(buf + op);
+  dp.kc = dp.pkc = reinterpret_cast<const uint16_t*>(buf + ok);
+  dp.kc_mul = dp.pkc_mul = reinterpret_cast<const float*>(buf + oe);
+  dp.v = dp.pv = reinterpret_cast<const __nv_bfloat16*>(buf + ov);
+  dp.lens = reinterpret_cast<const int*>(buf + ol);
+  dp.out = reinterpret_cast<__nv_bfloat16*>(buf + oo);
+  dp.pcap = plen;
+  dp.ws = buf + ow;
+  if (!st) st = run_decode_shared(dp, nullptr, static_cast<unsigned long long>(limit_ms) * 1000000ull, 1);
+  if (!st) st = cuda_status(cudaDeviceSynchronize());
+  int word = 0;
+  if (!st) st = cuda_status(cudaMemcpy(&word, err, sizeof word, cudaMemcpyDeviceToHost));
+  const int zero = 0;
+  if (!st) st = cuda_status(cudaMemcpy(err, &zero, sizeof zero, cudaMemcpyHostToDevice));
+  cudaFree(buf);
+  if (st) return st;
+  return word ? SPA_ERR_TIMEOUT : SPA_OK;
+}
+
 int spa_device_error(int* code) {
   if (!code) return SPA_ERR_NULL;
   int* p = nullptr;

@@ -201,3 +201,11 @@ def test_binding_refuses_host_tensors():
         pkg.spa_attention_decode_shared(q[:, :, 0], q, q, q, q, q)
     with pytest.raises(ValueError):
         pkg.spa_kcache_evict(q, q, q, q, q, q, 1)
+
+
+def test_decode_selftest_arguments():
+    pkg = spa()
+    assert pkg.selftest_decode_wait_timeout(0, 0) == SHAPE
+    assert pkg.selftest_decode_wait_timeout(2001, 1) == SHAPE
+    assert pkg.selftest_decode_wait_timeout(50, 2) == UNSUPPORTED
+    assert pkg.selftest_decode_wait_timeout(50, -1) == UNSUPPORTED

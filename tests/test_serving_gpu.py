@@ -2,6 +2,7 @@
 positions, ragged append, shared-prefix decode with weights, eviction, and a
 decode loop of all of them."""
 import math
+import time
 
 import numpy as np
 import pytest
@@ -671,3 +672,24 @@ def test_decode_loop():
                 assert {int(at[b]) - 1 - i for i in range(min(recent, n))} <= p
     # every step gave each sequence's own rows at most G of weight in all
     assert float(acc.sum(-1).max()) <= 12 * G + 1e-3
+
+
+@pytest.mark.parametrize("kernel", [0, 1])
+def test_decode_kernels_report_a_wait_that_runs_out(kernel):
+    """The prefix kernel withholds its first "scores ready", the kernel of the own
+    rows leaves its first copies unissued: the waits give up after 50 ms, every
+    role drains what it started, and the device error word reports it.  A decode
+    afterwards is right."""
+    pkg = spa()
+    t0 = time.perf_counter()
+    status = pkg.selftest_decode_wait_timeout(50, kernel)
+    elapsed = time.perf_counter() - t0
+    assert status == pkg.SPA_ERR_TIMEOUT, pkg.status_str(status)
+    assert elapsed < 1.5, f"self-test took {elapsed:.2f} s"
+    assert pkg.device_error() == 0
+    g = gen(77)
+    q, P = randn(g, 2, 4, 64, dtype=BF16), (randn(g, 1, 64, 32) / math.sqrt(32)).to(BF16)
+    cache = make_cache(g, 2, 1, 200, m=32, dv=64, d=64)
+    prefix = make_cache(g, 1, 1000, m=32, dv=64, d=64)
+    check_decode(pkg, q, P, cache, torch.tensor([200, 99], dtype=I32, device="cuda"), prefix, 1000,
+                 what="after the self-test")
