@@ -17,12 +17,17 @@
 //                        row that stays by a radix selection (or, for a few rows to
 //                        drop, those one by one); then the ranks of holes and of rows
 //                        to move, a lane per row
-//   evict_move_kernel    the rows' K~, multiplier and V, a warp per row, four rows
-//                        in flight
-// The first is bound by issued instructions, the second by memory.  Other selections
-// that were measured on 512 pairs of 2049 rows (18 us with the histogram): equal digits
-// of a warp counted by one lane 39 us, two bits per pass by counting keys above three
-// candidates 31 us.
+//   evict_move_kernel    the rows' K~, multiplier and V, a warp per row; many warps
+//                        with a row each in flight beat fewer with more (64 pairs of
+//                        up to 16383 rows: 52 us for the whole call, two rows 54, four
+//                        60, eight 71)
+// The first is bound by issued instructions and the latency of its passes, the second
+// by memory.  Dropping one of 2049 rows of 512 pairs: selection 9.5 us, move 4.7 us
+// (what it cannot do without: 3.1 us of memory traffic); 4096 of up to 16383 rows of
+// 64 pairs, which occupy 64 SMs in the selection: 46 us in all (traffic: 13.8 us).
+// Selections that were measured on 512 pairs of 2049 rows: a histogram of 8 bits per
+// pass 18 us, equal digits of a warp counted by one lane 39 us, two bits per pass by
+// counting keys above three candidates 31 us, the worst row looked for 9.5 us.
 #include "decode_shared.cuh"
 #include "kernels.cuh"
 
@@ -55,7 +60,7 @@ constexpr int kRegKeys = 16;  // rows per thread that fit in registers
 constexpr int kFew = 4;       // rows to drop that are looked for one by one
 
 template <int THREADS, Keys KEYS>
-__global__ void __launch_bounds__(THREADS) evict_select_kernel(const EvictParams p) {
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) evict_select_kernel(const EvictParams p) {
   extern __shared__ uint32_t dyn[];  // a bit per row that stays; kShared: the keys behind them
   constexpr int W = THREADS / 32;
   __shared__ alignas(16) int hist[2][256];
@@ -85,6 +90,7 @@ __global__ void __launch_bounds__(THREADS) evict_select_kernel(const EvictParams
   // A warp takes a run of 32-row words, w0 .. w1-1, a lane a row of each.
   const int words = (n + 31) / 32, per = (words + W - 1) / W;
   const int w0 = min(warp * per, words), w1 = min(w0 + per, words);
+  const int mine = w1 - w0, row0 = 32 * w0 + lane;
   uint32_t* const bits = dyn;
   uint32_t* const keys = dyn + (p.cap + 31) / 32;
   uint32_t reg[KEYS == kRegisters ? kRegKeys : 1];
@@ -95,7 +101,7 @@ __global__ void __launch_bounds__(THREADS) evict_select_kernel(const EvictParams
     if constexpr (KEYS == kRegisters) {
 #pragma unroll
       for (int e = 0; e < kRegKeys; ++e)
-        if (w0 + e < w1) f(w0 + e, 32 * (w0 + e) + lane, reg[e]);
+        if (e < mine) f(w0 + e, row0 + 32 * e, reg[e]);
     } else {
 #pragma unroll 4
       for (int w = w0; w < w1; ++w) {
@@ -109,8 +115,8 @@ __global__ void __launch_bounds__(THREADS) evict_select_kernel(const EvictParams
   if constexpr (KEYS == kRegisters) {
 #pragma unroll
     for (int e = 0; e < kRegKeys; ++e) {
-      const int i = 32 * (w0 + e) + lane;
-      const bool in = w0 + e < w1 && i < n;
+      const int i = row0 + 32 * e;
+      const bool in = e < mine && i < n;
       const int x = in ? pos[i] : -2147483647 - 1;
       weight[e] = in ? acc[i] : 0.f;
       reg[e] = static_cast<uint32_t>(x);
@@ -130,7 +136,7 @@ __global__ void __launch_bounds__(THREADS) evict_select_kernel(const EvictParams
   if constexpr (KEYS == kRegisters) {
 #pragma unroll
     for (int e = 0; e < kRegKeys; ++e)
-      reg[e] = w0 + e < w1 && 32 * (w0 + e) + lane < n ? key_of(weight[e], static_cast<int>(reg[e]), p.sink, last) : 0u;
+      reg[e] = e < mine && row0 + 32 * e < n ? key_of(weight[e], static_cast<int>(reg[e]), p.sink, last) : 0u;
   } else if constexpr (KEYS == kShared) {
 #pragma unroll 8
     for (int w = w0; w < w1; ++w) {
@@ -138,23 +144,36 @@ __global__ void __launch_bounds__(THREADS) evict_select_kernel(const EvictParams
       if (i < n) keys[i] = key_of(acc[i], pos[i], p.sink, last);  // read by this lane alone
     }
   }
-  // `low` and `want`: the rows of a larger key stay, and of those equal to it the
-  // first `want` (all of them: exact = false).
-  uint32_t low = 0;
-  int want = 0;
-  bool exact = true;
-  uint32_t keep = ~0u;  // the bits that are compared
   if (n - left <= kFew) {
     // The usual step drops a row: the worst rows one after the other, by smallest
-    // key and then last row.  The last of them to go has the key `low`.
+    // key and then last row.
+    const int drop = n - left;
     uint64_t gone = ~0ull;  // (key, row from the end) of the last one that went
-    int dropped = 0;        // of the key `low`
-    for (int round = 0; round < n - left; ++round) {
-      uint64_t worst = ~0ull;
-      each([&](int, int i, uint32_t k) {
-        const uint64_t x = static_cast<uint64_t>(k) << 32 | static_cast<uint32_t>(n - 1 - i);
-        if (i < n && x < worst && (round == 0 || x > gone)) worst = x;
-      });
+    int row[kFew];          // the rows that go; none: -1
+#pragma unroll
+    for (int r = 0; r < kFew; ++r) row[r] = -1;
+#pragma unroll 1
+    for (int round = 0; round < drop; ++round) {
+      uint32_t key = ~0u;
+      int at = -1;
+      if (round == 0) {
+        // a lane meets its rows in ascending order: an equal key goes to the later one
+        each([&](int, int i, uint32_t k) {
+          if (i < n && k <= key) {
+            key = k;
+            at = i;
+          }
+        });
+      } else {  // not those that went: smaller keys, and of the same key later rows
+        const uint32_t top = static_cast<uint32_t>(gone >> 32);
+        each([&](int, int i, uint32_t k) {
+          if (i < n && k <= key && (k > top || (k == top && i < row[0]))) {
+            key = k;
+            at = i;
+          }
+        });
+      }
+      uint64_t worst = at < 0 ? ~0ull : static_cast<uint64_t>(key) << 32 | static_cast<uint32_t>(n - 1 - at);
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) {
         const uint64_t x = __shfl_xor_sync(0xffffffffu, worst, o);
@@ -169,19 +188,55 @@ __global__ void __launch_bounds__(THREADS) evict_select_kernel(const EvictParams
         worst = x < worst ? x : worst;
       }
       gone = worst;
-      const uint32_t k = static_cast<uint32_t>(worst >> 32);
-      dropped = round > 0 && k == low ? dropped + 1 : 1;
-      low = k;
+#pragma unroll
+      for (int r = kFew - 1; r > 0; --r) row[r] = row[r - 1];  // the newest first
+      row[0] = n - 1 - static_cast<int>(worst & 0xffffffffu);
     }
-    // those equal to `low` that stay: all but the last `dropped` of them
-    int same = 0;
-    each([&](int, int i, uint32_t k) { same += i < n && k == low; });
-    same = __reduce_add_sync(0xffffffffu, same);
-    if (lane == 0) red2[0][warp] = make_int2(same, 0);
-    __syncthreads();
-    want = __reduce_add_sync(0xffffffffu, lane < W ? red2[0][lane].x : 0) - dropped;
-    __syncthreads();
-  } else {
+    // Every weight and position has been read.  The last `drop` rows: those of them
+    // that stay fill the places of the rows that go in front of them, in order.
+    auto goes = [&](int i) {
+      bool y = false;
+#pragma unroll
+      for (int r = 0; r < kFew; ++r) y |= i == row[r];
+      return y;
+    };
+    for (int i = tid; i < left; i += THREADS) {
+      if (goes(i)) continue;
+      src[i] = i;
+      if (acc_out != acc) acc_out[i] = acc[i];
+      if (pos_out != pos) pos_out[i] = pos[i];
+    }
+    if (tid < drop) {
+      const int i = left + tid;
+      int rank = 0;  // of this row among those to move
+      for (int x = left; x < i; ++x) rank += !goes(x);
+      if (!goes(i)) {
+        int to = -1;  // the place of that rank, in ascending order
+#pragma unroll
+        for (int r = 0; r < kFew; ++r) {
+          int lower = 0;
+#pragma unroll
+          for (int x = 0; x < kFew; ++x) lower += row[x] >= 0 && row[x] < row[r];
+          if (row[r] >= 0 && row[r] < left && lower == rank) to = row[r];
+        }
+        ws[4 + 2 * rank] = to;
+        ws[5 + 2 * rank] = i;
+        src[to] = i;
+        acc_out[to] = acc[i];
+        pos_out[to] = pos[i];
+        ++rank;
+      }
+      if (i == n - 1) ws[0] = rank;
+    }
+    return;
+  }
+  // `low` and `want`: the rows of a larger key stay, and of those equal to it the
+  // first `want` (all of them: exact = false).
+  uint32_t low = 0;
+  int want = 0;
+  bool exact = true;
+  uint32_t keep = ~0u;  // the bits that are compared
+  {
     // radix selection of the left-th largest key, 8 bits at a time until all keys of
     // the digit stay; below, keys are compared in the bits that were decided
     uint32_t mask = 0;
@@ -260,22 +315,39 @@ __global__ void __launch_bounds__(THREADS) evict_select_kernel(const EvictParams
     at.x += __popc(holes);
   }
   __syncthreads();  // the holes come before the rows that fill them
-#pragma unroll 4
-  for (int w = w0; w < w1; ++w) {
-    const int i = 32 * w + lane;
-    const uint32_t m = bits[w], movers = m & ~below(w);
-    if (m >> lane & 1u) {
-      int to = i;
-      if (movers >> lane & 1u) {
-        int* move = ws + 4 + 2 * (at.y + __popc(movers & lower));
-        to = move[0];
-        move[1] = i;
+  const bool copy_acc = acc_out != acc, copy_pos = pos_out != pos;
+  constexpr int E = 4;  // words whose loads are in flight together
+#pragma unroll 1
+  for (int v = w0; v < w1; v += E) {
+    int to[E], slot[E], x[E];
+    float a[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const int w = v + e, i = 32 * w + lane;
+      to[e] = slot[e] = -1;
+      if (w >= w1) continue;
+      const uint32_t m = bits[w], movers = m & ~below(w);
+      if (m >> lane & 1u) {
+        const bool moves = movers >> lane & 1u;
+        to[e] = i;
+        if (moves) {
+          slot[e] = 4 + 2 * (at.y + __popc(movers & lower));
+          to[e] = ws[slot[e]];
+        }
+        if (moves || copy_acc) a[e] = acc[i];
+        if (moves || copy_pos) x[e] = pos[i];
       }
-      src[to] = i;
-      if (to != i || acc_out != acc) acc_out[to] = acc[i];
-      if (to != i || pos_out != pos) pos_out[to] = pos[i];
+      at.y += __popc(movers);
     }
-    at.y += __popc(movers);
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const int i = 32 * (v + e) + lane;
+      if (to[e] < 0) continue;
+      src[to[e]] = i;
+      if (slot[e] >= 0) ws[slot[e] + 1] = i;
+      if (slot[e] >= 0 || copy_acc) acc_out[to[e]] = a[e];
+      if (slot[e] >= 0 || copy_pos) pos_out[to[e]] = x[e];
+    }
   }
 }
 
@@ -286,36 +358,26 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictPar
   const int bh = blockIdx.x / blocks, part = blockIdx.x % blocks;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int* ws = p.ws + static_cast<size_t>(bh) * evict_stride(p.cap, p.budget);
-  const int moves = ws[0];
   const int kp = p.m / 8, vp = p.dv / 8;  // 16-byte pieces of a row
   uint4* kc = reinterpret_cast<uint4*>(p.kc) + static_cast<size_t>(bh) * p.cap * kp;
   uint4* v = reinterpret_cast<uint4*>(p.v) + static_cast<size_t>(bh) * p.cap * vp;
   float* mul = p.kc_mul + static_cast<size_t>(bh) * p.cap;
   const int stride = blocks * (kMoveThreads / 32);
-  constexpr int E = 4;  // rows in flight
-  for (int i0 = part * (kMoveThreads / 32) + warp; i0 < moves; i0 += E * stride) {
-    int2 at[E];  // destination, source
-#pragma unroll
-    for (int e = 0; e < E; ++e)
-      if (i0 + e * stride < moves) at[e] = *reinterpret_cast<const int2*>(ws + 4 + 2 * (i0 + e * stride));
-    uint4 a[E], c[E];
-    float f[E];
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      if (i0 + e * stride >= moves) continue;
-      const size_t from = at[e].y;
-      if (lane < kp) a[e] = kc[from * kp + lane];
-      if (lane < vp) c[e] = v[from * vp + lane];
-      if (lane == 0) f[e] = mul[from];
-    }
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      if (i0 + e * stride >= moves) continue;
-      const size_t to = at[e].x;
-      if (lane < kp) kc[to * kp + lane] = a[e];
-      if (lane < vp) v[to * vp + lane] = c[e];
-      if (lane == 0) mul[to] = f[e];
-    }
+  const int moves = ws[0];
+  const int2* list = reinterpret_cast<const int2*>(ws + 4);  // destination, source
+  int i = part * (kMoveThreads / 32) + warp;
+  int2 next = i < moves ? list[i] : make_int2(0, 0);
+  for (; i < moves; i += stride) {
+    const size_t to = next.x, from = next.y;
+    uint4 k, x;
+    float f;
+    if (lane < kp) k = kc[from * kp + lane];
+    if (lane < vp) x = v[from * vp + lane];
+    if (lane == 0) f = mul[from];
+    if (i + stride < moves) next = list[i + stride];  // while the row is on its way
+    if (lane < kp) kc[to * kp + lane] = k;
+    if (lane < vp) v[to * vp + lane] = x;
+    if (lane == 0) mul[to] = f;
   }
   // one thread per sequence reads its length and writes the new one
   if (part == 0 && bh % p.H == 0 && threadIdx.x == 0) {
@@ -346,7 +408,7 @@ cudaError_t launch_evict(const EvictParams& p, cudaStream_t stream) {
                   : p.cap <= 49600           ? launch_select<1024, kShared>(p, stream)
                                              : launch_select<1024, kNowhere>(p, stream);
   if (e != cudaSuccess) return e;
-  const int blocks = (152 * 8 + p.B * p.H - 1) / (p.B * p.H);
+  const int blocks = (152 * 16 + p.B * p.H - 1) / (p.B * p.H);
   return ds::launch_after(evict_move_kernel, static_cast<unsigned>(p.B * p.H * blocks), kMoveThreads, 0, stream, p, blocks);
 }
 
