@@ -771,7 +771,7 @@ Geo geometry(const DecodeSharedParams& p, int sms) {
   g.rows = g.parts > 1 ? kTile : (p.B < g.spt ? p.B : g.spt) * p.G;
   g.PT = (p.plen + kTile - 1) / kTile;
   g.capr = (p.cap + kTile - 1) / kTile * kTile;
-  g.warp_own = p.G <= kOwnGroup;
+  g.warp_own = p.G <= kDecodeOwnGroup;
   g.ounit = g.warp_own ? kStep : kTile;
   const int opart = g.warp_own ? kStep : kTile;  // rows of an own part
   g.oparts = (p.G + opart - 1) / opart;

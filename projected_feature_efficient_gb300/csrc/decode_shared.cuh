@@ -23,7 +23,6 @@ namespace ds {
 
 constexpr int kTile = 128;          // keys per tile, rows per row tile
 constexpr int kStep = 16;           // keys per step of the own kernel, rows of its products
-constexpr int kOwnGroup = 32;       // largest group that the own kernel takes
 constexpr int kOwnWarps = 8;        // warps per CTA of the own kernel
 constexpr int kMaxCtas = 256;       // grid limit (sizes the workspace)
 constexpr int kPrefixSlots = 1024;  // prefix segments per call at most (beyond one per row tile)

@@ -56,8 +56,9 @@ __device__ __forceinline__ int2 warps_before(int2 v, int2* red) {
 
 // Where the keys are between the passes.
 enum Keys { kRegisters, kShared, kNowhere };
-constexpr int kRegKeys = 16;  // rows per thread that fit in registers
-constexpr int kFew = 4;       // rows to drop that are looked for one by one
+constexpr int kRegKeys = 16;        // rows per thread that fit in registers
+constexpr int kFew = 4;             // rows to drop that are looked for one by one
+constexpr int kSharedRows = 49600;  // rows whose keys fit in 200 KB of shared memory
 
 template <int THREADS, Keys KEYS>
 __global__ void __launch_bounds__(THREADS, 1024 / THREADS) evict_select_kernel(const EvictParams p) {
@@ -390,9 +391,12 @@ template <int THREADS, Keys KEYS>
 cudaError_t launch_select(const EvictParams& p, cudaStream_t stream) {
   const long long words = (p.cap + 31LL) / 32;
   const int smem = static_cast<int>(4 * (KEYS == kShared ? 33 * words : words));
-  const cudaError_t e = cudaFuncSetAttribute(evict_select_kernel<THREADS, KEYS>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
+  if (smem > 48 * 1024) {  // more than a launch may ask for as it is
+    static std::atomic<uint64_t> done{0};
+    constexpr int most = KEYS == kShared ? 4 * 33 * ((kSharedRows + 31) / 32) : kEvictMaxRows / 8;
+    const cudaError_t e = ds::allow_smem(evict_select_kernel<THREADS, KEYS>, most, done);
+    if (e != cudaSuccess) return e;
+  }
   evict_select_kernel<THREADS, KEYS><<<p.B * p.H, THREADS, smem, stream>>>(p);
   return cudaGetLastError();
 }
@@ -405,7 +409,7 @@ cudaError_t launch_evict(const EvictParams& p, cudaStream_t stream) {
   cudaError_t e = p.cap <= 256 * kRegKeys    ? launch_select<256, kRegisters>(p, stream)
                   : p.cap <= 512 * kRegKeys  ? launch_select<512, kRegisters>(p, stream)
                   : p.cap <= 1024 * kRegKeys ? launch_select<1024, kRegisters>(p, stream)
-                  : p.cap <= 49600           ? launch_select<1024, kShared>(p, stream)
+                  : p.cap <= kSharedRows     ? launch_select<1024, kShared>(p, stream)
                                              : launch_select<1024, kNowhere>(p, stream);
   if (e != cudaSuccess) return e;
   const int blocks = (152 * 16 + p.B * p.H - 1) / (p.B * p.H);

@@ -235,8 +235,11 @@ struct DecodeSharedParams {
 // the prefix [0] and the sequences' caches [1], with boxes of 128 and 16 rows of
 // at most 64 features; K~ fp16 in the swizzle of its box's row (32, 64 or 128
 // bytes), V bf16 in 128 bytes.
+// The sequences' own rows run on a kernel of their own for groups up to this (16-row
+// boxes alone), and on the prefix kernel for larger ones.
+constexpr int kDecodeOwnGroup = 32;
 struct DecodeSharedRun {
-  CUtensorMap k[2][2], v[2][2];
+  CUtensorMap k[2][2], v[2][2];  // prefix, own; boxes of 128 and of 16 rows
   int sms;
   int* err;                     // device error word
   unsigned long long limit_ns;  // time limit of every wait in the kernel

@@ -790,7 +790,7 @@ int run_decode_shared(const spa::DecodeSharedParams& dp, cudaStream_t stream,
   for (int own = 0; own < 2; ++own) {
     const int rows = own ? dp.cap : dp.plen, heads = own ? dp.B * dp.Hk : dp.Hk;
     if (rows == 0) continue;  // never loaded from
-    for (int small = 0; small < 2; ++small)
+    for (int small = own && dp.G <= spa::kDecodeOwnGroup; small < 2; ++small)
       if ((st = encode_cache_map(&run.k[own][small], own ? dp.kc : dp.pkc, dp.m,
                                  own ? dp.cap : dp.pcap, heads, small ? 16 : 128,
                                  CU_TENSOR_MAP_DATA_TYPE_FLOAT16)) ||
