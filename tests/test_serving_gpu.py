@@ -2,6 +2,7 @@
 positions, ragged append, shared-prefix decode with weights, eviction, and a
 decode loop of all of them."""
 import math
+import threading
 import time
 
 import numpy as np
@@ -234,6 +235,43 @@ def test_append_rows_outside_the_cache_are_not_written():
     assert bool((vc[~want[:, None]] == 0).all())
 
 
+def test_append_from_two_threads():
+    """Calls of two widths at the same time, on a stream each: one thread's launches
+    do not take the shared memory from the other's."""
+    pkg = spa()
+    B, H, T, m, dv, cap = 2, 2, 33, 128, 64, 40
+    pos = torch.zeros(B, dtype=I32, device="cuda")
+    work, errors = [], []
+    for i, d in enumerate((256, 33)):
+        g = gen(91 + i)
+        k, v = randn(g, B, H, T, d, dtype=BF16), randn(g, B, H, T, dv, dtype=BF16)
+        P = (randn(g, H, d, m) / math.sqrt(m)).to(BF16)
+        caches = [(torch.zeros((B, H, cap, m), dtype=torch.int16, device="cuda"),
+                   torch.zeros((B, H, cap), device="cuda"),
+                   torch.zeros((B, H, cap, dv), dtype=BF16, device="cuda")) for _ in range(2)]
+        work.append((k, v, P, caches, torch.cuda.Stream()))
+        pkg.spa_kcache_append_ragged(k, v, P, *caches[0], pos)
+    torch.cuda.synchronize()
+
+    def run(k, v, P, caches, stream):
+        try:
+            for _ in range(200):
+                pkg.spa_kcache_append_ragged(k, v, P, *caches[1], pos, stream=stream)
+        except Exception as e:  # told to the test's own thread
+            errors.append(e)
+
+    threads = [threading.Thread(target=run, args=w) for w in work]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not errors
+    for _, _, _, (a, b), _ in work:
+        for x, y in zip(a, b):
+            assert torch.equal(x, y)
+
+
 def test_append_multiplier_at_powers_of_two():
     """Row maxima on, just under and just over a power of two, by sums that fp32 rounds."""
     pkg = spa()
@@ -355,6 +393,10 @@ DECODE = [
     (1100, 2, 2, 64, 32, 64, 24, 300, [(5 * i) % 25 for i in range(1100)]),
     (70, 4, 4, 64, 16, 64, 2000, 0, [0] * 69 + [2000]),
     (70, 4, 4, 64, 32, 64, 2000, 6000, [2000] + [0] * 69),
+    # no rows of the sequences' own at all, with and without a prefix
+    (3, 4, 2, 64, 32, 64, 0, 700, [0, 0, 0]),
+    (2, 40, 1, 64, 32, 64, 0, 130, [0, 0]),
+    (2, 4, 2, 64, 32, 64, 0, 0, [0, 0]),
 ]
 
 
