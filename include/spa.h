@@ -372,8 +372,8 @@ SPA_API int spa_rope(const void *q, const void *k, void *q_out, void *k_out,
  *   sequence, with the value rows: of k [B][H][T][d] and v [B][H][T][d_v]
  *   (bf16; H key heads here) the first count[b] (NULL: T) rows go to cache
  *   rows pos[b] .. of kc, kc_mul and vc [B][H][cap][d_v].  Rows are as
- *   spa_kcache_append writes them, up to the order of the fp32 sums, with the
- *   multiplier of the exact row maximum.  For the eviction, the new rows of
+ *   spa_kcache_append writes them, up to the order of the fp32 sums; maxima
+ *   next to a power of two choose their multiplier by sums in 64 bits.  For the eviction, the new rows of
  *   acc [B][H][cap] are set to 0 and those of row_pos [B][H][cap] to token[b]
  *   + t (NULL: pos[b] + t); acc and row_pos may be NULL.  No two sequences
  *   share rows, so the calls of a graph replay bit for bit.
@@ -402,9 +402,11 @@ SPA_API int spa_kcache_append_ragged(const void *k, const void *v, const void *P
  *   workspace: device, 256-byte aligned, at least
  *   spa_attention_decode_shared_workspace_size bytes, overwritten, for this
  *   call alone until it has run; NULL: from the library's pool.
- *   Scores, softmax statistics and sums are fp32.  SPA_BF16 only; 1 <= d <=
- *   256, m in {16, 32, 64, 128}, d_v in {64, 128}, H a multiple of Hk,
- *   B*H <= 65535.
+ *   Scores, softmax statistics, sums and the weights are fp32 (the projected
+ *   query enters with 22 bits); probabilities are rounded to bf16 for the value
+ *   product, and the output to bf16.  Multipliers are powers of two, as the
+ *   appends write them.  SPA_BF16 only; 1 <= d <= 256, m in {16, 32, 64, 128},
+ *   d_v in {64, 128}, H a multiple of Hk, B*H <= 65535.
  */
 SPA_API int spa_attention_decode_shared_workspace_size(int B, int H, int Hk, int plen, int d,
                                                        int m, int d_v, int cap, int weights,
