@@ -780,15 +780,19 @@ Geo geometry(const DecodeSharedParams& p, int sms) {
   const long long own = static_cast<long long>(p.Hk) * p.B * g.oparts * ((p.cap + g.ounit - 1LL) / g.ounit);
   const long long all = rowtiles * g.PT + (g.warp_own ? 0 : own);
   g.grid = static_cast<int>(all < 1 ? 1 : all < most ? all : most);
-  // the split of the prefix with the shortest schedule: rounds of segments,
-  // each its tiles and about two tiles' time of start and end
+  // the split of the prefix with the shortest schedule, in cycles: rounds of segments,
+  // each its tiles and about two tiles' time of start and end, and the partial sums'
+  // way to memory and back (65536 keys for 512 rows of 8 key heads: 4, 9, 14, 19, 28
+  // segments per row tile 258, 251, 256, 259, 270 us for the whole call)
   if (g.PT > 0) {
+    const long long tile = p.m <= 32 ? 1750 : p.m == 64 ? 2400 : 3500;
+    const long long sums = rowtiles * g.rows * p.dv * 8 / 3500;
     long long best = -1;
     long long limit = kPrefixSlots / rowtiles;
     limit = limit < 1 ? 1 : limit > g.PT ? g.PT : limit;
     for (int s = 1; s <= limit; ++s) {
       const int chunk = (g.PT + s - 1) / s, S = (g.PT + chunk - 1) / chunk;
-      const long long cost = (rowtiles * S + g.grid - 1) / g.grid * (chunk + 2);
+      const long long cost = (rowtiles * S + g.grid - 1) / g.grid * (chunk + 2) * tile + S * sums;
       if (best < 0 || cost < best) {
         best = cost;
         g.S = S;
