@@ -17,6 +17,7 @@ using namespace ptx;
 // largest magnitude in [2^13, 2^14) and two fp16 parts (22 bits).  A CTA takes 16
 // rows of a row tile: thread = (column, run of features), P_h read once per CTA.
 // The last CTA counts the own tiles in front of every sequence.
+// Bound by latency: 5 us for 1024 rows (d = 128, m = 32), 8 us for 4096 (m = 64).
 constexpr int kQueryThreads = 256, kQueryRows = 16;
 
 __device__ void count_tiles(const Params& a, int* red) {
@@ -165,6 +166,11 @@ __global__ void __launch_bounds__(kQueryThreads) decode_query_kernel(const __gri
 // products are an eighth of the time that the bytes take.  (The same rows on
 // tcgen05, 128 rows for a group of 4, took 4 times as long: each short segment
 // drains the scores, the sums and their output in turn.)
+// 128 sequences of 0 to 2047 rows, 8 key heads (m = 64, d_v = 128): 77 us, 412 MB read
+// at 5.4 TB/s; 16 sequences of 17 to 8191 rows, 4 key heads (m = 32): 17 us for 85 MB.
+// Behind a prefix kernel its CTAs move in as that one's leave; with SMs of its own
+// beside the prefix kernel and runs taken as warps came, the calls took longer (32768
+// shared keys: 49 us for 45, 65536: 283 for 257).
 template <int M, int DV>
 struct OwnPlan {
   static constexpr int kV = kStep * DV * 2, kK = kStep * M * 2;
@@ -482,6 +488,10 @@ __device__ __forceinline__ float2 stats_of(const Params& a, const Parts& x, int 
   return *reinterpret_cast<const float2*>(p);
 }
 
+// Bound by the latency of a row's chain (lengths, statistics, sums) where there are few
+// rows, and by issued instructions with weights: 7 us for 1024 rows of 19 + 1 parts, 24
+// us for 4096 rows and 4.2 million weights (45 MB read).  One, two or eight warps per
+// row: 13, 7 and 8 us, and 23, 26 and 32 us.
 // Four warps per row of the output (the first `oblocks` blocks), each a quarter
 // of its partial results, a lane per DV/32 of its columns.  The other blocks:
 // the weights of 1024 keys of a (sequence, key head).

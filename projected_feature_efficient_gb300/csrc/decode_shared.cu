@@ -46,6 +46,19 @@
 // is never used.  A segment's sums start afresh, so that one sequence's values
 // never meet another's rows.
 //
+// What bounds it.  65536 keys against 512 rows of each of 8 key heads (m = 64, d_v =
+// 128): 148 us, 2450 cycles per tile and row tile; the products alone would take 1070
+// (the score product's K is 2 m for the two parts of q~).  A tile moves 176 KB through
+// the SM's shared memory, 1400 cycles at 128 bytes a cycle: both operands of the score
+// product, V, what TMA writes and the range pass.  The issuer is held up by the tensor
+// pipe for 1600 cycles of a tile and waits for probabilities for 630.  32768 keys
+// against 128 rows (m = 32): 28 us, 1750 cycles per tile, which is the memory
+// bandwidth, and 10000 + 6000 cycles of start and end.  One score buffer that both
+// streams read into registers, with the probabilities beside it and the scores three
+// tiles ahead, took the softmax out of the way between two score products, and the
+// large case took 266 us for 251: the issuer then waited for nothing, and each product
+// took longer.
+//
 // Every wait is bounded; a role that gives up sets the CTA's abort flag and
 // the device error word, and all roles leave after their own operations in
 // flight have ended.
