@@ -95,8 +95,14 @@ __device__ __forceinline__ void stage_projection(uint2* frag, const __nv_bfloat1
   }
 }
 
+// CTAs per SM: as many as the registers of 128 features in flight allow, and all of a
+// call's CTAs resident at once, so that P_h is staged once (m = 32, prompts: 4 per SM in
+// two waves 31 us, in one 33, 5 in one wave 27, 6 spill a little: 31).
 template <int M>
-__global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p, int tiles) {
+constexpr int kCtas = M <= 32 ? 5 : M == 64 ? 4 : 3;
+
+template <int M>
+__global__ void __launch_bounds__(kThreads, kCtas<M>) append_kernel(const AppendParams p, int tiles) {
   extern __shared__ uint2 frag[];
   const int h = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int q = lane & 3, r0 = lane >> 2;
@@ -267,7 +273,7 @@ cudaError_t launch(const AppendParams& p, cudaStream_t stream) {
   const cudaError_t e = ds::allow_smem(append_kernel<M>, 256 * M * 2, done);
   if (e != cudaSuccess) return e;
   long long blocks = (tiles + kWarps - 1) / kWarps;
-  const long long most = (152LL * 8 + p.H - 1) / p.H;
+  const long long most = (152LL * kCtas<M> + p.H - 1) / p.H;
   if (blocks > most) blocks = most;
   append_kernel<M><<<dim3(static_cast<unsigned>(blocks), p.H), kThreads, smem, stream>>>(
       p, static_cast<int>(tiles));
