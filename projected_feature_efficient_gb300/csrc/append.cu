@@ -14,11 +14,14 @@
 // to the neighbouring power, which fp16 holds as well).
 //
 // Bound by memory for long prompts: keys and values are read once and K~ and
-// values written once.  4 x 4095 rows of 8 heads (d = d_v = 128, m = 32): 23 us,
-// 3.6 TB/s (82 MB; 12.1 us at the measured 6.8 TB/s); 64 sequences' one row each:
-// 6 us, two round trips to memory behind the launch.  A warp holds 16 rows' keys in
-// registers as the A fragments, so a row needs one load and no staging; with P_h
-// staged element by element and values after the keys the prompts took 33 us.
+// values written once.  4 x up to 4095 rows of 8 heads (d = d_v = 128, m = 32; 82
+// MB, 12.1 us at the measured 6.8 TB/s): the kernel 18 to 20 us, 4.3 TB/s; in a
+// stream of calls 28 to 37 us, which changes with the process and so with where the
+// buffers lie.  64 sequences' one row each: 6 us, two round trips to memory behind
+// the launch.  A warp holds 16 rows' keys in registers as the A fragments, so a row
+// needs one load and no staging; value rows are copied by CTAs of their own, whose
+// loads wait for nothing else.  With P_h staged element by element and the values
+// behind the keys in the same warps the prompts took 33 us.
 #include <math.h>
 
 #include "decode_shared.cuh"
@@ -95,74 +98,71 @@ __device__ __forceinline__ void stage_projection(uint2* frag, const __nv_bfloat1
   }
 }
 
-// CTAs per SM: as many as the registers of 128 features in flight allow, and all of a
-// call's CTAs resident at once, so that P_h is staged once (m = 32, prompts: 4 per SM in
-// two waves 31 us, in one 33, 5 in one wave 27, 6 spill a little: 31).
+// CTAs per SM, half of them for the keys and half for the value rows: as many as the
+// registers of 128 features in flight allow, and all of a call's CTAs resident at once,
+// so that P_h is staged once.  (m = 32, the prompts below in a graph: 25 us; 8 or 10 per
+// SM in more than one wave 31 and 37; keys and values in the same warps, 5 per SM 27,
+// 4 per SM in two waves 31.)
 template <int M>
-constexpr int kCtas = M <= 32 ? 5 : M == 64 ? 4 : 3;
+constexpr int kCtas = M <= 32 ? 6 : M == 64 ? 4 : 3;
 
 template <int M>
 __global__ void __launch_bounds__(kThreads, kCtas<M>) append_kernel(const AppendParams p, int tiles) {
   extern __shared__ uint2 frag[];
   const int h = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int q = lane & 3, r0 = lane >> 2;
+  const long long R = static_cast<long long>(p.B) * p.T;
+  // where row r comes from (a row of k and v) and goes to; false: nowhere
+  auto place = [&](long long r, long long* from, long long* dst, int* b, int* t) {
+    if (r >= R) return false;
+    *b = static_cast<int>(r / p.T);
+    *t = static_cast<int>(r - static_cast<long long>(*b) * p.T);
+    const long long at = static_cast<long long>(p.pos[*b]) + *t;
+    if ((p.count && *t >= p.count[*b]) || at < 0 || at >= p.cap) return false;
+    *from = (static_cast<long long>(*b) * p.H + h) * p.T + *t;
+    *dst = (static_cast<long long>(*b) * p.H + h) * p.cap + at;
+    return true;
+  };
+  if (blockIdx.z == 1) {
+    // value rows, 16 per warp and turn: a lane a piece of 16 bytes of two or four rows at
+    // a time, all of the tile in flight; the lanes 0-15 (and 16-31) know a row each
+    constexpr int kPieces = 8;
+    const int pieces = p.dv / 8;  // per row: 8 or 16
+    for (int tile = blockIdx.x * kWarps + warp; tile < tiles; tile += gridDim.x * kWarps) {
+      long long from = 0, dst = -1;
+      int b, t;
+      place(static_cast<long long>(tile) * 16 + (lane & 15), &from, &dst, &b, &t);
+      uint4 v[kPieces];
+#pragma unroll
+      for (int e = 0; e < kPieces; ++e) {
+        const int at = 32 * e + lane, row = at / pieces;
+        const long long s = __shfl_sync(0xffffffffu, from, row & 15), d = __shfl_sync(0xffffffffu, dst, row & 15);
+        if (row < 16 && d >= 0) v[e] = __ldg(reinterpret_cast<const uint4*>(p.v + s * p.dv) + at % pieces);
+      }
+#pragma unroll
+      for (int e = 0; e < kPieces; ++e) {
+        const int at = 32 * e + lane, row = at / pieces;
+        const long long d = __shfl_sync(0xffffffffu, dst, row & 15);
+        if (row < 16 && d >= 0) *(reinterpret_cast<uint4*>(p.vc + d * p.dv) + at % pieces) = v[e];
+      }
+    }
+    return;
+  }
   const int groups = (p.d + 31) / 32;
   const __nv_bfloat16* P = p.P + static_cast<size_t>(h) * p.d * M;
   stage_projection<M>(frag, P, p.d, groups, tid);
   __syncthreads();
-  const long long R = static_cast<long long>(p.B) * p.T;
   const bool wide = p.d % 8 == 0;
-  // Value rows: lanes take the tile's rows two (four) at a time, a piece of 16 bytes
-  // each; where a row comes from and goes to is known to the lanes that have it.
-  constexpr int kPieces = 4;
-  const int pieces = p.dv / 8;  // per row: 8 or 16
-  auto piece_of = [&](int i, int* row) {
-    const int at = 32 * i + lane;
-    *row = at / pieces;
-    return at - *row * pieces;
-  };
-  auto row_of = [&](const long long (&x)[2], int row) {
-    const long long a = __shfl_sync(0xffffffffu, x[0], (row & 7) * 4), b = __shfl_sync(0xffffffffu, x[1], (row & 7) * 4);
-    return row < 8 ? a : b;
-  };
-  auto load_values = [&](const long long (&from)[2], const long long (&dst)[2], int i0, uint4 (&v)[kPieces]) {
-#pragma unroll
-    for (int e = 0; e < kPieces; ++e) {
-      int row;
-      const int piece = piece_of(i0 + e, &row);
-      const long long s = row_of(from, row), t = row_of(dst, row);
-      if (t >= 0) v[e] = __ldg(reinterpret_cast<const uint4*>(p.v + s * p.dv) + piece);
-    }
-  };
-  auto store_values = [&](const long long (&dst)[2], int i0, const uint4 (&v)[kPieces]) {
-#pragma unroll
-    for (int e = 0; e < kPieces; ++e) {
-      int row;
-      const int piece = piece_of(i0 + e, &row);
-      const long long t = row_of(dst, row);
-      if (t >= 0) *(reinterpret_cast<uint4*>(p.vc + t * p.dv) + piece) = v[e];
-    }
-  };
   for (int tile = blockIdx.x * kWarps + warp; tile < tiles; tile += gridDim.x * kWarps) {
-    // this lane's two rows: where they come from (a row of k and v) and where they go
-    // (-1: nowhere)
-    long long from[2], dst[2];
+    long long from[2], dst[2];  // this lane's two rows
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const long long r = static_cast<long long>(tile) * 16 + r0 + 8 * i;
       from[i] = 0;
       dst[i] = -1;
-      if (r < R) {
-        const int b = static_cast<int>(r / p.T), t = static_cast<int>(r - static_cast<long long>(b) * p.T);
-        const long long at = static_cast<long long>(p.pos[b]) + t;
-        if ((!p.count || t < p.count[b]) && at >= 0 && at < p.cap) {
-          from[i] = (static_cast<long long>(b) * p.H + h) * p.T + t;
-          dst[i] = (static_cast<long long>(b) * p.H + h) * p.cap + at;
-          if (q == 0) {
-            if (p.acc) p.acc[dst[i]] = 0.f;
-            if (p.row_pos) p.row_pos[dst[i]] = (p.token ? p.token[b] : p.pos[b]) + t;
-          }
-        }
+      int b, t;
+      if (place(static_cast<long long>(tile) * 16 + r0 + 8 * i, &from[i], &dst[i], &b, &t) && q == 0) {
+        if (p.acc) p.acc[dst[i]] = 0.f;
+        if (p.row_pos) p.row_pos[dst[i]] = (p.token ? p.token[b] : p.pos[b]) + t;
       }
     }
     if (!__any_sync(0xffffffffu, dst[0] >= 0 || dst[1] >= 0)) continue;
@@ -172,8 +172,6 @@ __global__ void __launch_bounds__(kThreads, kCtas<M>) append_kernel(const Append
     for (int j = 0; j < M / 8; ++j)
 #pragma unroll
       for (int e = 0; e < 4; ++e) c[j][e] = 0.f;
-    uint4 vp[kPieces];  // the value rows' first pieces, in flight with the keys
-    load_values(from, dst, 0, vp);
     for (int g0 = 0; g0 < groups; g0 += 4) {  // 128 features in flight
       uint4 w[4][2];
 #pragma unroll
@@ -206,10 +204,6 @@ __global__ void __launch_bounds__(kThreads, kCtas<M>) append_kernel(const Append
           }
         }
       }
-    }
-    for (int i = 0; i < pieces / 2; i += kPieces) {  // the value rows, 16 bytes per lane
-      if (i > 0) load_values(from, dst, i, vp);
-      store_values(dst, i, vp);
     }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -273,9 +267,9 @@ cudaError_t launch(const AppendParams& p, cudaStream_t stream) {
   const cudaError_t e = ds::allow_smem(append_kernel<M>, 256 * M * 2, done);
   if (e != cudaSuccess) return e;
   long long blocks = (tiles + kWarps - 1) / kWarps;
-  const long long most = (152LL * kCtas<M> + p.H - 1) / p.H;
+  const long long most = (152LL * kCtas<M> / 2 + p.H - 1) / p.H;
   if (blocks > most) blocks = most;
-  append_kernel<M><<<dim3(static_cast<unsigned>(blocks), p.H), kThreads, smem, stream>>>(
+  append_kernel<M><<<dim3(static_cast<unsigned>(blocks), p.H, 2), kThreads, smem, stream>>>(
       p, static_cast<int>(tiles));
   return cudaGetLastError();
 }
