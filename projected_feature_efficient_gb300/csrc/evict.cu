@@ -18,9 +18,9 @@
 //                        drop, those one by one); then the ranks of holes and of rows
 //                        to move, a lane per row
 //   evict_move_kernel    the rows' K~, multiplier and V, a warp per row; many warps
-//                        with a row each in flight beat fewer with more (64 pairs of
-//                        up to 16383 rows, caches flushed: 52 us for the whole call, two rows 54, four
-//                        60, eight 71)
+//                        with a row each in flight beat fewer with more (64 pairs
+//                        of up to 16383 rows, caches flushed: 52 us for the whole
+//                        call, two rows 54, four 60, eight 71)
 // The first is bound by issued instructions and the latency of its passes, the second
 // by memory.  Dropping one of 2049 rows of 512 pairs: selection 9.5 us, move 4.7 us
 // (what it cannot do without: 3.1 us of memory traffic); 4096 of up to 16383 rows of
