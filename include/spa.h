@@ -403,8 +403,9 @@ SPA_API int spa_kcache_append_ragged(const void *k, const void *v, const void *P
  *   spa_attention_decode_shared_workspace_size bytes, overwritten, for this
  *   call alone until it has run; NULL: from the library's pool.
  *   Scores, softmax statistics, sums and the weights are fp32 (the projected
- *   query enters with 22 bits); probabilities are rounded to bf16 for the value
- *   product, and the output to bf16.  Multipliers are powers of two, as the
+ *   query enters with 22 bits).  For the value product the probabilities of a
+ *   sequence's own rows keep 16 bits, and those of the prefix (and of own rows
+ *   where H / Hk > 32) are rounded to bf16; the output is bf16.  Multipliers are powers of two, as the
  *   appends write them.  SPA_BF16 only; 1 <= d <= 256, m in {16, 32, 64, 128},
  *   d_v in {64, 128}, H a multiple of Hk, B*H <= 65535.
  */

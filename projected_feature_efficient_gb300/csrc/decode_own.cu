@@ -161,9 +161,11 @@ __global__ void __launch_bounds__(kQueryThreads) decode_query_kernel(const __gri
 // for itself: K~ and V by TMA (16-row boxes, swizzled for ldmatrix) and the
 // multipliers by 4-byte copies into a ring of its own, S = q~ K~^T and O += P V by
 // mma.sync with the group's heads as the 16 rows (a group of more than 16: two
-// parts), softmax in registers as in the prefix kernel.  The rows that 16 heads
-// cannot fill cost nothing here: reading the cache bounds the kernel, and the
-// products are an eighth of the time that the bytes take.  (The same rows on
+// parts), softmax in registers as in the prefix kernel.  Probabilities enter the value
+// product in two bf16 parts, 16 bits: an output is off by its own rounding alone, as in
+// the decode of one length (one part: 33.9 us for 35.1, on the 16 sequences below with
+// their weights).  The rows that 16 heads cannot fill cost nothing here: reading the
+// cache bounds the kernel, and the products are a fifth of the time that the bytes take.  (The same rows on
 // tcgen05, 128 rows for a group of 4, took 4 times as long: each short segment
 // drains the scores, the sums and their output in turn.)
 // 128 sequences of 0 to 2047 rows, 8 key heads (m = 64, d_v = 128): 77 us, 412 MB read
@@ -200,6 +202,12 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], 
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Two values as bf16 pairs of high and low parts, which add up to them within 2^-16.
+__device__ __forceinline__ void split_bf16x2(float x, float y, uint32_t& hi, uint32_t& lo) {
+  hi = pack_bf16x2(x, y);
+  lo = pack_bf16x2(x - __uint_as_float(hi << 16), y - __uint_as_float(hi & 0xffff0000u));
 }
 
 // A place in the order (key head, sequence, part, key) of the own rows.
@@ -390,8 +398,9 @@ __device__ __forceinline__ void run_own(const Params& a, const Maps& maps, uint8
       l0 += s[h][0] + s[h][1];
       l1 += s[h][2] + s[h][3];
     }
-    const uint32_t p[4] = {pack_bf16x2(s[0][0], s[0][1]), pack_bf16x2(s[0][2], s[0][3]),
-                           pack_bf16x2(s[1][0], s[1][1]), pack_bf16x2(s[1][2], s[1][3])};
+    uint32_t p[4], pl[4];  // probabilities in two parts
+#pragma unroll
+    for (int e = 0; e < 4; ++e) split_bf16x2(s[e >> 1][2 * (e & 1)], s[e >> 1][2 * (e & 1) + 1], p[e], pl[e]);
 #pragma unroll
     for (int c = 0; c < DV / 16; ++c) {
       const int key = lane & 15, piece = 2 * c + (lane >> 4);
@@ -399,6 +408,8 @@ __device__ __forceinline__ void run_own(const Params& a, const Maps& maps, uint8
       ldsm4t(b, vs + (piece >> 3) * 2048 + key * 128 + (((piece & 7) ^ (key & 7)) << 4));
       mma_bf16(o[2 * c], p, b[0], b[1]);
       mma_bf16(o[2 * c + 1], p, b[2], b[3]);
+      mma_bf16(o[2 * c], pl, b[0], b[1]);
+      mma_bf16(o[2 * c + 1], pl, b[2], b[3]);
     }
     if (n < kStep) fence_proxy_async_smem();  // zeroed rows, which a copy overwrites next
     __syncwarp();  // every lane has read the slot

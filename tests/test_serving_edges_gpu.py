@@ -1,0 +1,88 @@
+"""The serving operators at their edges, on the GPU against 64-bit arithmetic."""
+import math
+import os
+
+import numpy as np
+import pytest
+import torch
+
+from helpers import ROOT, spa
+from test_serving_gpu import (BF16, F32, I32, U, gen, make_cache, no_wait_ran_out, projected,  # noqa: F401
+                              randn, run_evict)
+
+pytestmark = pytest.mark.gpu
+
+
+# ------------------------------------------------------------------ shared-prefix decode
+def exact_decode(q, P, cache, lens, prefix=None):
+    """Outputs and weights in 64 bits, and how far fp32 scores, probabilities and sums may be from
+    them, key by key: a key counts by its own probability."""
+    B, H, d = q.shape
+    Hk, _, m = P.shape
+    kc, mul, v = cache
+    out = torch.zeros((B, H, v.shape[-1]), dtype=torch.float64, device="cuda")
+    tol = torch.zeros_like(out)
+    weights = torch.zeros(kc.shape[:3], dtype=torch.float64, device="cuda")
+    wtol = torch.zeros_like(weights)
+    lens = lens.tolist()
+    for b in range(B):
+        for h in range(H):
+            hk, n = h // (H // Hk), lens[b]
+            K = kc[b, hk, :n].view(torch.float16).double() * mul[b, hk, :n, None].double()
+            V = v[b, hk, :n].double()
+            if prefix is not None:
+                K = torch.cat((prefix[0][hk].view(torch.float16).double() * prefix[1][hk, :, None].double(), K))
+                V = torch.cat((prefix[2][hk].double(), V))
+            if len(K) == 0:
+                continue
+            s = (q[b, h].double() @ P[hk].double()) @ K.T / math.sqrt(m)
+            p = torch.softmax(s, -1)
+            mag = q[b, h].double().abs() @ P[hk].double().abs()
+            # a score: d and m fp32 products and sums, counted as 2(d + m) + 8 roundings of the sum of
+            # magnitudes; the query in 22 bits of its largest entry (2^-23 each); the key's entries to
+            # 2^-24 of its largest; four roundings on the way to its exponential
+            off = (mag @ K.abs().T * (2 * d + 2 * m + 8) * 2.0 ** -24 +
+                   mag.max() * (K.abs().sum(-1) * 2.0 ** -23 + m * K.abs().amax(-1) * 2.0 ** -24)) / math.sqrt(m)
+            rel = torch.expm1(torch.clamp(off, max=1.0)) + 4 * 2.0 ** -24 * (s.abs() + s.max().abs()) + 2.0 ** -20
+            all_ = (p * rel).sum()
+            # probabilities in two bf16 parts (2^-16), on the prefix kernel in one (2^-8); sums of 16
+            # products each
+            one = torch.full_like(p, 2.0 ** -16)
+            one[:len(K) if H // Hk > 32 else len(K) - n] = 2.0 ** -8
+            out[b, h] = p @ V
+            tol[b, h] = (p * (rel + one)) @ V.abs() + (all_ + (len(K) / 16 + 64) * 2.0 ** -23) * (p @ V.abs())
+            weights[b, hk, :n] += p[len(K) - n:]
+            wtol[b, hk, :n] += (p * (rel + all_ + (len(K) / 16 + 64) * 2.0 ** -23))[len(K) - n:]
+    return out, 1.01 * tol, weights, 1.01 * wtol
+
+
+def check_exact(pkg, q, P, cache, lens, prefix=None, weights=True):
+    acc = torch.zeros(cache[1].shape, device="cuda") if weights else None
+    got = pkg.spa_attention_decode_shared(q, P, *cache, lens, prefix=prefix, acc=acc)
+    out, tol, want, wtol = exact_decode(q, P, cache, lens, prefix)
+    over = (got.double() - out).abs() - (U[BF16] * (out.abs() + tol) + tol + 1e-30)
+    assert float(over.max()) <= 0, f"{float(over.max())} over, of {float(out.abs().max())}"
+    if weights and acc.numel():
+        inside = torch.arange(acc.shape[2], device="cuda")[None, None] < lens[:, None, None]
+        over = (acc.double() - want).abs() - wtol - 4 * q.shape[1] / P.shape[0] * U[F32] * want - 1e-30
+        assert float(over[inside.expand_as(over)].amax() if bool(inside.any()) else 0) <= 0
+    return got
+
+
+@pytest.mark.parametrize("shape", [
+    # B, H, Hk, d, m, dv, lens: few keys, so that each one's probability shows
+    (3, 4, 2, 64, 32, 64, [40, 7, 1]),
+    (16, 8, 8, 64, 16, 64, [5 + i for i in range(16)]),
+    (4, 8, 1, 128, 64, 128, [24, 3, 17, 30]),
+    (8, 4, 4, 128, 128, 128, [17, 5] * 4),
+    (3, 32, 1, 64, 32, 128, [33, 9, 4]),
+])
+def test_decode_probabilities_keep_their_bits(shape):
+    """On the sequences' own rows an output is off by its own rounding alone, not by the
+    probabilities'."""
+    pkg = spa()
+    B, H, Hk, d, m, dv, lens = shape
+    g = gen(B + H + m)
+    q, P = randn(g, B, H, d, dtype=BF16), (randn(g, Hk, d, m) / math.sqrt(m)).to(BF16)
+    cache = make_cache(g, B, Hk, 40, m=m, dv=dv, d=d)
+    check_exact(pkg, q, P, cache, torch.tensor(lens, dtype=I32, device="cuda"))
