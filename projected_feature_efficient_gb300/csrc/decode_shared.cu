@@ -27,11 +27,13 @@
 //
 // Scores.  q~ comes split into two fp16 parts (22 bits), so the scores carry
 // fp32's precision.  The cache rows are fp16 with a power of two each; a warp
-// brings the rows of a tile to the largest of them in shared memory (exact: a row
-// only loses bits where it is 2^14 times smaller than another, and then below
-// fp16's rounding of that one), and the tile's common factor joins the row's.
-// (With a multiplication per score instead, read from shared memory, the softmax
-// of a tile took 600 cycles more, of 2200.)  K~ and V have rings of their own
+// brings the rows of a tile to the largest multiplier of them in shared memory, and
+// the tile's common factor joins the row's.  A row's largest entry is 2^13 or more, so
+// down to a factor of 2^-14 its entries lose less than 2^-24 of it (what falls below
+// fp16's 2^-24 is rounded); where a tile's multipliers are further apart, as beside a
+// row of zeros, whose multiplier is 1, the rows stay as they are and the softmax takes
+// each score by its own key's.  (That for every tile, read from shared memory, made the
+// softmax of a tile 600 cycles longer, of 2200.)  K~ and V have rings of their own
 // because a K~ slot is free again once the scores are formed; with both in one slot
 // the way from a free slot to scores that can be formed took 3500 cycles, and with
 // the three slots that fit at m = 64 a tile took 2300.
@@ -88,7 +90,8 @@ constexpr int kLoadWarp = 12, kMmaWarp = 13;
 constexpr int kSegs = 8;               // segments the scheduler may be ahead
 constexpr int kSegReaders = 1 + 2 + 4 + 8;  // issuer, multipliers, output warps, softmax warps
 constexpr float kSumLimit = 1099511627776.f;  // 2^40
-constexpr int kMaxDynSmem = 227 * 1024 - 9 * 1024;
+constexpr int kMaxDynSmem = 227 * 1024 - 10 * 1024;
+constexpr float kRange = 1.f / 16384.f;  // 2^-14: what the rows of a tile may be apart for one range
 
 constexpr int cmax(int a, int b) { return a > b ? a : b; }
 
@@ -130,11 +133,15 @@ struct Shared {
   volatile int abort;
   Seg seg[kSegs];
   float stat_l[2][2][kTile], stat_m[2][2][kTile];
-  float mul[2][3][kTile];
-  float kscale[16];  // by the tile's number: no warp is that many tiles behind
+  // by the tile's number: a K~ slot is filled again once the scores of the tile that was
+  // in it are formed, six tiles behind at most, and those wait until the softmax is done
+  // with the tile two in front; so no reader is eight tiles behind
+  alignas(16) float mul[8][kTile];
+  float kscale[8];  // 0: the rows of the tile keep their own multipliers
 };
 static_assert(offsetof(Shared, seg) % 16 == 0 && alignof(Shared) >= 16, "vector loads from shared memory");
-static_assert(sizeof(Shared) <= 9 * 1024 - 256, "static shared memory");
+static_assert(sizeof(Shared) <= 10 * 1024 - 256, "static shared memory");
+static_assert(offsetof(Shared, mul) % 16 == 0, "vector loads from shared memory");
 
 // The CTA's segments in order, then the end: told to the other roles, then given
 // to `load`.
@@ -381,7 +388,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
               const int k = lane + 32 * c;
-              float* to = &sh.mul[mine][slot][k];
+              float* to = &sh.mul[at % 8][k];
               if (k < n)
                 asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(to)), "l"(from + k) : "memory");
               else
@@ -403,7 +410,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (issued == done && !fetch(true)) break;
         while (issued < done + KS && fetch(false)) {
         }
-        const int slot = done % KS;
+        const int slot = done % KS, tile = (2 * done + mine) % 8;
         if (issued == done + 3)
           asm volatile("cp.async.wait_group 2;" ::: "memory");
         else if (issued == done + 2)
@@ -412,9 +419,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           asm volatile("cp.async.wait_group 0;" ::: "memory");
         float x[4];  // each lane reads what it copied
 #pragma unroll
-        for (int c = 0; c < 4; ++c) x[c] = sh.mul[mine][slot][lane + 32 * c];
+        for (int c = 0; c < 4; ++c) x[c] = sh.mul[tile][lane + 32 * c];
         // rows behind the length have the multiplier 0 here; 1 where there is none
-        const float top = warp_max(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])));
+        // (positive floats are in the order of their bits)
+        int most = 0;
+        uint32_t least = ~0u;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          most = max(most, __float_as_int(x[c]));
+          least = min(least, __float_as_uint(x[c]) - 1u);  // 0 is no multiplier
+        }
+        const float top = __int_as_float(__reduce_max_sync(0xffffffffu, most));
+        const float low = __uint_as_float(__reduce_min_sync(0xffffffffu, least) + 1u);
+        const bool narrow = low >= top * kRange;
         const float scale = top > 0.f ? top : 1.f, inv = __frcp_rn(scale);
         if (!__all_sync(0xffffffffu, wait_or_abort(&sh.k_full[mine][slot], (done / KS) & 1, ctl))) break;
         // the lanes' rows lie 32, 64 or 128 bytes apart: each starts at another piece of
@@ -423,7 +440,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           const float f = x[c] * inv;
-          if (__any_sync(0xffffffffu, f != 1.f)) {  // row lane + 32 c, all of it by one factor
+          if (narrow && __any_sync(0xffffffffu, f != 1.f)) {  // row lane + 32 c, all of it by one factor
             const __half2 h = __float2half2_rn(f);
             uint8_t* row = ring + slot * P::kKBytes + (lane + 32 * c) * P::kKRow;
             constexpr int kBatch = M / 8 < 8 ? M / 8 : 8;  // 16-byte pieces in flight
@@ -444,7 +461,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
-        if (lane == 0) sh.kscale[(2 * done + mine) % 16] = scale;
+        if (lane == 0) sh.kscale[tile] = narrow ? scale : 0.f;
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.k_ready[mine][slot]);
@@ -663,6 +680,26 @@ __global__ void __launch_bounds__(kThreads, 1)
           fence_proxy_async_smem();
         }
         if (here) {
+          const float ks = sh.kscale[at % 8];
+          if (ks == 0.f) {  // each key's own multiplier
+            const float4* km = reinterpret_cast<const float4*>(sh.mul[at % 8]);
+#pragma unroll 1
+            for (int c = 0; c < 128; c += 32) {
+              uint32_t v[32];
+              tmem_ld32(tS + c, v);
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 32; e += 4) {
+                const float4 f = km[(c + e) / 4];
+                v[e] = __float_as_uint(__uint_as_float(v[e]) * (qm * f.x));
+                v[e + 1] = __float_as_uint(__uint_as_float(v[e + 1]) * (qm * f.y));
+                v[e + 2] = __float_as_uint(__uint_as_float(v[e + 2]) * (qm * f.z));
+                v[e + 3] = __float_as_uint(__uint_as_float(v[e + 3]) * (qm * f.w));
+              }
+              tmem_st32(tS + c, v);
+            }
+            tmem_wait_st();
+          }
           float x[128];
           {
             uint32_t v0[32], v1[32], v2[32], v3[32];
@@ -679,7 +716,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               x[96 + c] = __uint_as_float(v3[c]);
             }
           }
-          const float mult = qm * sh.kscale[at % 16];  // > 0
+          const float mult = ks == 0.f ? 1.f : qm * ks;  // > 0
           if (n < kTile) {
 #pragma unroll
             for (int c = 0; c < 128; ++c) x[c] = c < n ? x[c] : -INFINITY;

@@ -86,3 +86,74 @@ def test_decode_probabilities_keep_their_bits(shape):
     q, P = randn(g, B, H, d, dtype=BF16), (randn(g, Hk, d, m) / math.sqrt(m)).to(BF16)
     cache = make_cache(g, B, Hk, 40, m=m, dv=dv, d=d)
     check_exact(pkg, q, P, cache, torch.tensor(lens, dtype=I32, device="cuda"))
+
+
+def rows_of(x):
+    """Rows as the appends write them: fp16 bits and a power of two, 1 for a row of zeros."""
+    top = x.abs().amax(-1)
+    mul = torch.where(top > 0, torch.exp2((torch.frexp(top)[1] - 14).double()), torch.ones_like(top))
+    return (x / mul[..., None]).to(torch.float16).view(torch.int16), mul.float()
+
+
+@pytest.mark.parametrize("kind", ["zero rows", "a far larger row", "all kinds"])
+@pytest.mark.parametrize("own", [False, True])
+@pytest.mark.parametrize("m", [16, 32, 64, 128])
+def test_decode_keys_of_other_magnitudes_in_a_tile(m, own, kind):
+    """Small keys keep their scores beside rows of zeros (multiplier 1) and beside rows 2^25 as
+    large: in the prefix, and in the own rows of a group that runs on the prefix kernel."""
+    pkg = spa()
+    g = gen(m + own)
+    B, H, Hk, d, dv, n = (1, 40, 1, 64, 64, 300) if own else (3, 8, 2, 64, 64, 300)
+    # queries of 2^14 against keys of 2^-14: scores of a few units
+    one = randn(g, 1, 1, d)
+    q = ((one + 0.3 * randn(g, B, H, d)) * 2.0 ** 14).to(BF16)
+    P = (randn(g, Hk, d, m) / math.sqrt(m)).to(BF16)
+    x = torch.randn((Hk, n, m), generator=g, device="cuda", dtype=torch.float64) * math.sqrt(d / m) * 2.0 ** -14
+    if kind == "all kinds":  # and rows down to 2^-30 of that: any factor within a tile
+        x[:, 140:] *= torch.exp2(-torch.randint(0, 31, (Hk, n - 140, 1), generator=g, device="cuda").double())
+    if kind != "a far larger row":
+        x[:, [3, 130, n - 1]] = 0
+    if kind != "zero rows":  # against all queries: its own probability is 0
+        far = torch.einsum("d,hdm->hm", one[0, 0].double(), P.double())
+        x[:, 17] = -2.0 ** 11 * far
+    kc, mul = rows_of(x)
+    v = randn(g, Hk, n, dv, dtype=BF16)
+    if own:
+        cache, prefix = (kc[None], mul[None], v[None]), None
+        lens = torch.tensor([n], dtype=I32, device="cuda")
+    else:
+        cache = make_cache(g, B, Hk, 8, m=m, dv=dv, d=d)
+        cache[1].mul_(2.0 ** -14)
+        prefix, lens = (kc, mul, v), torch.tensor([8, 0, 5], dtype=I32, device="cuda")
+    check_exact(pkg, q, P, cache, lens, prefix)
+
+
+@pytest.mark.parametrize("own", [False, True])
+@pytest.mark.parametrize("m", [16, 64, 128])
+def test_decode_scores_that_grow_along_the_keys(m, own):
+    """Later tiles of the prefix kernel move a row's maximum: its sums follow."""
+    pkg = spa()
+    g = gen(60 + m)
+    B, H, Hk, d, dv, n = (1, 40, 1, 64, 128, 1500) if own else (3, 8, 2, 64, 128, 1500)
+    q, P = randn(g, B, H, d, dtype=BF16), (randn(g, Hk, d, m) / math.sqrt(m)).to(BF16)
+    x = torch.randn((Hk, n, m), generator=g, device="cuda", dtype=torch.float64) * math.sqrt(d / m)
+    x *= torch.exp2(torch.arange(n, device="cuda").double()[:, None] // 250)  # up to 2^5
+    kc, mul = rows_of(x)
+    v = randn(g, Hk, n, dv, dtype=BF16)
+    if own:
+        cache, prefix = (kc[None], mul[None], v[None]), None
+        lens = torch.tensor([n], dtype=I32, device="cuda")
+    else:
+        cache = make_cache(g, B, Hk, 20, m=m, dv=dv, d=d)
+        prefix, lens = (kc, mul, v), torch.tensor([20, 0, 5], dtype=I32, device="cuda")
+    check_exact(pkg, q, P, cache, lens, prefix)
+
+
+def test_decode_long_own_caches():
+    """Own caches of 131072 and 32769 rows, and of one."""
+    pkg = spa()
+    g = gen(70)
+    B, H, Hk, d, m, dv, cap = 3, 4, 2, 128, 32, 128, 131072
+    q, P = randn(g, B, H, d, dtype=BF16), (randn(g, Hk, d, m) / math.sqrt(m)).to(BF16)
+    cache = make_cache(g, B, Hk, cap, m=m, dv=dv, d=d)
+    check_exact(pkg, q, P, cache, torch.tensor([cap, 32769, 1], dtype=I32, device="cuda"))
