@@ -391,7 +391,8 @@ template <int THREADS, Keys KEYS>
 cudaError_t launch_select(const EvictParams& p, cudaStream_t stream) {
   const long long words = (p.cap + 31LL) / 32;
   const int smem = static_cast<int>(4 * (KEYS == kShared ? 33 * words : words));
-  if (smem > 48 * 1024) {  // more than a launch may ask for as it is
+  if constexpr (KEYS != kRegisters) {
+    // the longest cache's for every call: 48 KB without asking count the static part in
     static std::atomic<uint64_t> done{0};
     constexpr int most = KEYS == kShared ? 4 * 33 * ((kSharedRows + 31) / 32) : kEvictMaxRows / 8;
     const cudaError_t e = ds::allow_smem(evict_select_kernel<THREADS, KEYS>, most, done);

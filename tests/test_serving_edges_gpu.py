@@ -157,3 +157,14 @@ def test_decode_long_own_caches():
     q, P = randn(g, B, H, d, dtype=BF16), (randn(g, Hk, d, m) / math.sqrt(m)).to(BF16)
     cache = make_cache(g, B, Hk, cap, m=m, dv=dv, d=d)
     check_exact(pkg, q, P, cache, torch.tensor([cap, 32769, 1], dtype=I32, device="cuda"))
+
+
+# ------------------------------------------------------------------ eviction
+@pytest.mark.parametrize("cap", [380000, 1 << 20])
+def test_evict_longest_caches(cap):
+    """A bit per row in shared memory: 46 to 128 KB, with the kernel's own beside it."""
+    pkg = spa()
+    g = gen(cap)
+    acc = torch.floor(torch.rand((1, 1, cap), generator=g, device="cuda") * 5000)
+    row_pos = torch.argsort(torch.rand((1, 1, cap), generator=g, device="cuda"), dim=-1).to(I32)
+    run_evict(pkg, g, 1, 1, 16, 64, cap, cap - 5000, 4, 300, [cap - 1], acc, row_pos, True)
