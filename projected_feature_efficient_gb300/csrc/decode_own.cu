@@ -170,9 +170,11 @@ __global__ void __launch_bounds__(kQueryThreads) decode_query_kernel(const __gri
 // drains the scores, the sums and their output in turn.)
 // 128 sequences of 0 to 2047 rows, 8 key heads (m = 64, d_v = 128): 77 us, 412 MB read
 // at 5.4 TB/s; 16 sequences of 17 to 8191 rows, 4 key heads (m = 32): 17 us for 85 MB.
-// Behind a prefix kernel its CTAs move in as that one's leave; with SMs of its own
-// beside the prefix kernel and runs taken as warps came, the calls took longer (32768
-// shared keys: 49 us for 45, 65536: 283 for 257).
+// Behind a prefix kernel it waits for that one's end (moving in as its CTAs left took 47
+// us for 50 with 32768 shared keys and 255 for 262 with 65536, but read the queries and
+// offsets without the wait that makes another kernel's results visible).  With SMs of
+// its own beside the prefix kernel and runs taken as warps came, the calls took longer
+// than that (49 and 283).
 template <int M, int DV>
 struct OwnPlan {
   static constexpr int kV = kStep * DV * 2, kK = kStep * M * 2;
@@ -451,14 +453,11 @@ __global__ void __launch_bounds__(32 * kOwnWarps, 1)
   if (lane < P::kStages) mbar_init(&full[warp][lane], 1 + 32);  // the bytes, and every lane's multipliers
   fence_mbar_init();
   __syncwarp();
-  // Behind the prefix kernel this one starts when every CTA there has seen the
-  // query kernel's results, and does not wait for the rest of it: its CTAs move
-  // in where those have left.  The wait at the end makes the combine kernel's
-  // wait for this kernel one for both.
-  if (a.g.units == 0) wait_for_previous();
+  // The query kernel's results are seen after this wait alone, also behind a prefix
+  // kernel that has waited for them itself.
+  wait_for_previous();
   let_next_start();
   run_own<M, DV>(a, maps, smem_raw, full[warp], mul[warp]);
-  if (a.g.units > 0) wait_for_previous();
 }
 
 // ------------------------------------------------------------------- combine
@@ -645,6 +644,8 @@ cudaError_t launch_own_m(const Params& a, const Maps& maps, cudaStream_t stream)
 
 }  // namespace
 
+// A plain launch, behind everything in the stream: the kernels that follow load the
+// caches and write the workspace without waiting for more than this one.
 cudaError_t launch_query(const Params& a, cudaStream_t stream) {
   const int slices = (a.g.rows + kQueryRows - 1) / kQueryRows;
   const unsigned grid = static_cast<unsigned>(a.p.Hk) * a.g.RT * slices + 1;

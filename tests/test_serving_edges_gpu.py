@@ -168,3 +168,26 @@ def test_evict_longest_caches(cap):
     acc = torch.floor(torch.rand((1, 1, cap), generator=g, device="cuda") * 5000)
     row_pos = torch.argsort(torch.rand((1, 1, cap), generator=g, device="cuda"), dim=-1).to(I32)
     run_evict(pkg, g, 1, 1, 16, 64, cap, cap - 5000, 4, 300, [cap - 1], acc, row_pos, True)
+
+
+def test_decode_one_workspace_with_changing_queries_and_lengths():
+    """Calls one behind the other on one workspace, without a pause: each sees the queries and
+    lengths of its own call."""
+    pkg = spa()
+    g = gen(80)
+    B, H, Hk, d, m, dv, cap, plen, calls = 24, 8, 2, 64, 32, 64, 700, 3000, 60
+    P = (randn(g, Hk, d, m) / math.sqrt(m)).to(BF16)
+    cache, prefix = make_cache(g, B, Hk, cap, m=m, dv=dv, d=d), make_cache(g, Hk, plen, m=m, dv=dv, d=d)
+    ws = torch.empty(pkg.spa_attention_decode_shared_workspace_size(B, H, Hk, plen, d, m, dv, cap),
+                     dtype=torch.uint8, device="cuda")
+    qs = randn(g, calls, B, H, d, dtype=BF16)
+    lens = torch.randint(0, cap + 1, (calls, B), generator=g, device="cuda", dtype=I32)
+    outs = torch.empty((calls, B, H, dv), dtype=BF16, device="cuda")
+    torch.cuda.synchronize()
+    for i in range(calls):
+        pkg.spa_attention_decode_shared(qs[i], P, *cache, lens[i], prefix=prefix, out=outs[i], workspace=ws)
+    torch.cuda.synchronize()
+    for i in range(calls):
+        want = pkg.spa_attention_decode_shared(qs[i], P, *cache, lens[i], prefix=prefix)
+        torch.cuda.synchronize()
+        assert torch.equal(outs[i], want), i
