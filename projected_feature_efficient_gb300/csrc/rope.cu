@@ -8,9 +8,10 @@
 //
 // The angle never goes through floating point before it is reduced: the table
 // holds f_i / 2pi as a 64-bit fraction of a turn, and position * table wraps
-// modulo one turn exactly in integer arithmetic.  Its top 32 bits, as a signed
-// fraction, are the angle to within 2^-32 of a turn at any position (an fp32
-// product is off by 2^-24 of the angle itself: 0.06 rad at position 10^6).
+// modulo one turn exactly in integer arithmetic.  Its top 48 bits, as a signed
+// fraction, are the angle to within 2^-48 of a turn at any position (an fp32
+// product is off by 2^-24 of the angle itself: 0.06 rad at position 10^6), so that
+// sine and cosine are off by their fp32 arithmetic alone.
 //
 // Bound by memory: every feature is read and written once.  A thread owns the
 // same vector of pairs in several heads of one token, so the sines are formed
@@ -50,11 +51,15 @@ __device__ __forceinline__ void sincos_of(const RopeParams& p, int pair, int pos
                                           float& c) {
   const unsigned long long turn =
       static_cast<unsigned long long>(static_cast<long long>(pos)) * p.table[pair];
-  // signed fraction of a turn in [-1/2, 1/2): angle / pi = 2 * fraction
-  const float half_turns = static_cast<float>(static_cast<int>(turn >> 32)) * 0x1p-31f;
-  sincospif(half_turns, &s, &c);
-  s *= p.scale;
-  c *= p.scale;
+  // signed fraction of a turn in [-1/2, 1/2): angle / pi = 2 * fraction.  Its first 24
+  // bits as a float, without rounding; the next 24 turn the result by the angle that is
+  // left, below pi 2^-23, whose square is nothing here.
+  const float half_turns = static_cast<float>(static_cast<int>(turn >> 32) & ~0xff) * 0x1p-31f;
+  const float rest = static_cast<float>(static_cast<uint32_t>(turn >> 16) & 0xffffffu) * (3.14159265f * 0x1p-47f);
+  float s0, c0;
+  sincospif(half_turns, &s0, &c0);
+  s = fmaf(rest, c0, s0) * p.scale;
+  c = fmaf(-rest, s0, c0) * p.scale;
   if (p.inverse) s = -s;
 }
 

@@ -191,3 +191,24 @@ def test_decode_one_workspace_with_changing_queries_and_lengths():
         want = pkg.spa_attention_decode_shared(qs[i], P, *cache, lens[i], prefix=prefix)
         torch.cuda.synchronize()
         assert torch.equal(outs[i], want), i
+
+
+# ------------------------------------------------------------------ rotary positions
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_rope_angle(interleaved):
+    """The angle to 2^-32 of a turn: near half turns, where the sine shows it."""
+    pkg = spa()
+    g = gen(90)
+    d, N = 64, 8192
+    table = pkg.rope_table(pkg.rope_frequencies(d))
+    pos = torch.randint(-(1 << 20), 1 << 20, (1, N), generator=g, device="cuda", dtype=I32)
+    x = torch.zeros((1, 1, N, d), device="cuda")
+    a, b = (slice(0, d, 2), slice(1, d, 2)) if interleaved else (slice(0, d // 2), slice(d // 2, d))
+    x[..., a] = 1.0
+    y = pkg.spa_rope(x, table, pos, interleaved=interleaved)
+    # the table's fraction of a turn, in wrapping 64-bit integers as the entry says
+    turn = pos[0, :, None].to(torch.int64) * table
+    angle = turn.double() * (2 * math.pi * 2.0 ** -64)
+    # 2 pi 2^-32 for the angle, the sine and cosine to 2 steps of fp32
+    for got, want in ((y[0, 0][:, a], torch.cos(angle)), (y[0, 0][:, b], torch.sin(angle))):
+        assert bool(((got.double() - want).abs() <= 2 * math.pi * 2.0 ** -32 + 4 * U[F32] * want.abs()).all())
