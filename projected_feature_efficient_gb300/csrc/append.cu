@@ -8,17 +8,20 @@
 // row alone.
 //
 // The row multiplier 2^e puts the row's largest magnitude in [2^13, 2^14).
-// Where the fp32 maximum is within 2^-17 of a power of two, which side it is
-// on is decided on sums in 64 bits, so that the multiplier is the exact one
-// (unless the row's sums cancel to below 2^-7 of their terms: then it may belong
-// to the neighbouring power, which fp16 holds as well).
+// Where the fp32 maximum is within 2^-12 of a power of two, which side it is
+// on is decided on 64-bit sums of the columns that are as near, so that the
+// multiplier is the exact one unless the row's sums cancel to below 2^-6 of their
+// terms: 256 features are 16 products of 16 features one after the other, each
+// off by 2^-22 of the terms at most, 2^-18 in all.  Beyond that it may belong to
+// the neighbouring power, which fp16 holds as well.
 //
 // Bound by memory for long prompts: keys and values are read once and K~ and
 // values written once.  4 x up to 4095 rows of 8 heads (d = d_v = 128, m = 32; 82
-// MB, 12.1 us at the measured 6.8 TB/s): the kernel 18 to 20 us, 4.3 TB/s; in a
-// stream of calls 28 to 37 us, which changes with the process and so with where the
-// buffers lie.  64 sequences' one row each: 6 us, two round trips to memory behind
-// the launch.  A warp holds 16 rows' keys in registers as the A fragments, so a row
+// MB, 12.1 us at the measured 6.8 TB/s): 22.7 us a call in a stream of calls, 3.6
+// TB/s.  The 64-bit sums are dealt out over a warp's lanes, feature by feature, for the
+// columns that need them alone; with a column per lane and all features one after the
+// other a row took longer than the rest of its warp's work, and the calls 30 to 39 us.
+// 64 sequences' one row each: 6 us, two round trips to memory behind the launch.  A warp holds 16 rows' keys in registers as the A fragments, so a row
 // needs one load and no staging; value rows are copied by CTAs of their own, whose
 // loads wait for nothing else.  With P_h staged element by element and the values
 // behind the keys in the same warps the prompts took 33 us.
@@ -33,6 +36,7 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
+constexpr uint32_t kNear = 2048;  // 2^-12 in fp32 steps above a power of two; half as far in steps below it
 
 __device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }
 
@@ -100,7 +104,8 @@ __device__ __forceinline__ void stage_projection(uint2* frag, const __nv_bfloat1
 
 // CTAs per SM, half of them for the keys and half for the value rows: as many as the
 // registers of 128 features in flight allow, and all of a call's CTAs resident at once,
-// so that P_h is staged once.  (m = 32, the prompts below in a graph: 25 us; 8 or 10 per
+// so that P_h is staged once.  (m = 32, the prompts above in a graph, with the slower
+// sums: 25 us; 8 or 10 per
 // SM in more than one wave 31 and 37; keys and values in the same warps, 5 per SM 27,
 // 4 per SM in two waves 31.)
 template <int M>
@@ -213,24 +218,40 @@ __global__ void __launch_bounds__(kThreads, kCtas<M>) append_kernel(const Append
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
       int e = row_exponent(top);
-      // rows whose maximum is next to a power of two: exact sums decide
+      // rows whose maximum is next to a power of two: exact sums decide (below 2^-110 all
+      // have the smallest multiplier)
       const uint32_t mant = __float_as_uint(top) & 0x7fffffu;
-      const bool near = dst[i] >= 0 && top > 0.f && isfinite(top) && (mant < 64u || mant > 0x7fffffu - 64u);
-      uint32_t todo = __ballot_sync(0xffffffffu, near && q == 0);
+      const bool near = dst[i] >= 0 && top > 0x1p-110f && isfinite(top) &&
+                        (mant < kNear || mant > 0x7fffffu - 2 * kNear);
+      uint32_t todo = __ballot_sync(0xffffffffu, near && q == 0), cols = 0;  // this lane's columns as near
+      if (near) {
+        float edge = __uint_as_float(__float_as_uint(top) & 0x7f800000u);
+        if (mant >= kNear) edge *= 2.f;
+#pragma unroll
+        for (int j = 0; j < M / 4; ++j)
+          if (fabsf(fabsf(c[j / 2][2 * i + j % 2]) - edge) <= edge * 0x1.1p-12f) cols |= 1u << j;
+      }
       while (todo) {
         const int from = __ffs(todo) - 1;
         todo &= todo - 1;
         const __nv_bfloat16* xr = reinterpret_cast<const __nv_bfloat16*>(
             __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(x[i]), from));
         double best = 0.0;
-        for (int n = lane; n < M; n += 32) {
-          double s = 0.0;
-          for (int k = 0; k < p.d; ++k)
-            s += static_cast<double>(__bfloat162float(xr[k])) * static_cast<double>(__bfloat162float(P[k * M + n]));
-          best = fmax(best, fabs(s));
-        }
+#pragma unroll 1
+        for (int g = 0; g < 4; ++g) {
+          uint32_t left = __shfl_sync(0xffffffffu, cols, from + g);
+#pragma unroll 1
+          for (; left; left &= left - 1) {
+            const __nv_bfloat16* Pn = P + g * (M / 4) + __ffs(left) - 1;
+            double s = 0.0;
+#pragma unroll 1
+            for (int k = lane; k < p.d; k += 32)
+              s += static_cast<double>(__bfloat162float(xr[k])) * static_cast<double>(__bfloat162float(Pn[k * M]));
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) best = fmax(best, __shfl_xor_sync(0xffffffffu, best, o));
+            for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+            best = fmax(best, fabs(s));
+          }
+        }
         if ((lane >> 2) == (from >> 2)) e = row_exponent(best);
       }
       if (dst[i] < 0) continue;

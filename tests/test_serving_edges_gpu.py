@@ -212,3 +212,30 @@ def test_rope_angle(interleaved):
     # 2 pi 2^-32 for the angle, the sine and cosine to 2 steps of fp32
     for got, want in ((y[0, 0][:, a], torch.cos(angle)), (y[0, 0][:, b], torch.sin(angle))):
         assert bool(((got.double() - want).abs() <= 2 * math.pi * 2.0 ** -32 + 4 * U[F32] * want.abs()).all())
+
+
+# ------------------------------------------------------------------ ragged append
+@pytest.mark.parametrize("terms", [16, 60])
+@pytest.mark.parametrize("d", [256, 200])
+def test_append_multiplier_of_cancelling_sums(d, terms):
+    """Row maxima just beside a power of two, to which d terms of up to 60 times that in all cancel."""
+    pkg = spa()
+    g = torch.Generator().manual_seed(d)
+    m, T = 32, 400
+    n = d // 2 - 2
+    r = torch.rand((T, n), generator=g, dtype=torch.float64) + 0.5
+    r *= torch.exp2(-torch.randint(0, 16, (T, n), generator=g).double())  # so that fp32 sums round
+    r = (r * ((terms - 1.2) / 2 / r.sum(-1, keepdim=True))).to(BF16).double()
+    k = torch.zeros((T, d), dtype=torch.float64)
+    k[:, 2:n + 2], k[:, n + 2:2 * n + 2] = r, -r                  # sums grow first and shrink then
+    k[:, 0] = 1.0
+    k[:, 1] = torch.exp2(-(torch.arange(T) % 12) - 15.0) * torch.where(torch.rand(T, generator=g) < 0.5, 1.0, -1.0)
+    k = k.to(BF16)[None, None].cuda()
+    P = torch.zeros((1, d, m), device="cuda", dtype=BF16)
+    P[0, :, 5] = 1.0
+    kc, mul = pkg.kcache_new(1, 1, T, m)
+    vc = torch.zeros((1, 1, T, 64), dtype=BF16, device="cuda")
+    pkg.spa_kcache_append_ragged(k, vc.clone(), P, kc, mul, vc, torch.zeros(1, dtype=I32, device="cuda"))
+    x, want, mag = projected(k, P)
+    assert float((mag.amax(-1) / x.abs().amax(-1)).max()) < 1.01 * terms
+    assert torch.equal(mul.double(), want)
