@@ -105,9 +105,8 @@ __device__ __forceinline__ void stage_projection(uint2* frag, const __nv_bfloat1
 // CTAs per SM, half of them for the keys and half for the value rows: as many as the
 // registers of 128 features in flight allow, and all of a call's CTAs resident at once,
 // so that P_h is staged once.  (m = 32, the prompts above in a graph, with the slower
-// sums: 25 us; 8 or 10 per
-// SM in more than one wave 31 and 37; keys and values in the same warps, 5 per SM 27,
-// 4 per SM in two waves 31.)
+// sums: 25 us; 8 or 10 per SM in more than one wave 31 and 37; keys and values in the
+// same warps, 5 per SM 27, 4 per SM in two waves 31.)
 template <int M>
 constexpr int kCtas = M <= 32 ? 6 : M == 64 ? 4 : 3;
 

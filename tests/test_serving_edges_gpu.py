@@ -239,3 +239,25 @@ def test_append_multiplier_of_cancelling_sums(d, terms):
     x, want, mag = projected(k, P)
     assert float((mag.amax(-1) / x.abs().amax(-1)).max()) < 1.01 * terms
     assert torch.equal(mul.double(), want)
+
+
+# ------------------------------------------------------------------ the README's step
+def test_readme_decode_steps():
+    """The README's loop: every new row has a position of its own, the next one."""
+    pkg = spa()
+    text = open(os.path.join(ROOT, "README.md")).read()
+    code = next(c for c in text.split("```python\n")[1:] if "spa_rope" in c).split("```")[0]
+    g = gen(99)
+    B, H, Hk, d, m, dv, cap, plen, n = 2, 4, 2, 64, 32, 64, 300, 50, 5
+    kc, kc_mul, vc = make_cache(g, B, Hk, cap, m=m, dv=dv, d=d)
+    names = dict(d=d, P=(randn(g, Hk, d, m) / math.sqrt(m)).to(BF16), kc=kc, kc_mul=kc_mul, vc=vc, budget=256,
+                 prefix=make_cache(g, Hk, plen, m=m, dv=dv, d=d), acc=torch.zeros((B, Hk, cap), device="cuda"),
+                 row_pos=torch.zeros((B, Hk, cap), dtype=I32, device="cuda"),
+                 lens=torch.zeros(B, dtype=I32, device="cuda"), pos=torch.tensor([plen, plen + 7], dtype=I32, device="cuda"),
+                 steps=[[randn(g, B, h, 1, c, dtype=BF16) for h, c in ((H, d), (Hk, d), (Hk, dv))] for _ in range(n)])
+    exec(code, names)
+    assert names["lens"].tolist() == [n, n]
+    for b, first in enumerate((plen, plen + 7)):
+        for h in range(Hk):
+            assert names["row_pos"][b, h, :n].tolist() == list(range(first, first + n))
+    assert bool(torch.isfinite(names["out"]).all())
