@@ -338,7 +338,9 @@ __device__ __forceinline__ void run_own(const Params& a, const Maps& maps, uint8
       }
       __syncwarp();
     }
-    // scores of keys 0-7 and 8-15: high parts of q~, then low parts
+    // scores of keys 0-7 and 8-15.  The low parts of q~ come first, while the sums are
+    // small: the sums that are rounded at the scores' size are the high parts' alone
+    uint32_t kf[M / 16][4];
     float s[2][4] = {};
 #pragma unroll
     for (int k = 0; k < M / 16; ++k) {
@@ -350,12 +352,14 @@ __device__ __forceinline__ void run_own(const Params& a, const Maps& maps, uint8
         addr = ks + key * 64 + ((piece ^ ((key >> 1) & 3)) << 4);
       else
         addr = ks + key * 32 + ((piece ^ ((key >> 2) & 1)) << 4);
-      uint32_t b[4];
-      ldsm4(b, addr);
-      mma_f16(s[0], qf[k], b[0], b[1]);
-      mma_f16(s[1], qf[k], b[2], b[3]);
-      mma_f16(s[0], qf[M / 16 + k], b[0], b[1]);
-      mma_f16(s[1], qf[M / 16 + k], b[2], b[3]);
+      ldsm4(kf[k], addr);
+      mma_f16(s[0], qf[M / 16 + k], kf[k][0], kf[k][1]);
+      mma_f16(s[1], qf[M / 16 + k], kf[k][2], kf[k][3]);
+    }
+#pragma unroll
+    for (int k = 0; k < M / 16; ++k) {
+      mma_f16(s[0], qf[k], kf[k][0], kf[k][1]);
+      mma_f16(s[1], qf[k], kf[k][2], kf[k][3]);
     }
     float t0 = -INFINITY, t1 = -INFINITY;
 #pragma unroll
@@ -583,7 +587,7 @@ __global__ void __launch_bounds__(kCombineThreads)
   const int w = blockIdx.x - oblocks, bh = dk(w), b = a.g.dHk(bh), hk = bh - b * a.p.Hk;
   const int n = length_of(a, b), k0 = (w - bh * kblocks) * 1024;
   if (k0 >= n) return;
-  __shared__ float lse[128];
+  __shared__ float2 stat[128];  // maximum, one over the sum
   constexpr int E = 1024 / kCombineThreads;
   float acc[E];
 #pragma unroll
@@ -603,7 +607,7 @@ __global__ void __launch_bounds__(kCombineThreads)
         sum = sum * ex2(top - now) + warp_sum(st.y > 0.f ? ex2(st.x - now) * st.y : 0.f);
         top = now;
       }
-      if (lane == 0) lse[g] = top + log2f(sum);
+      if (lane == 0) stat[g] = make_float2(top, 1.f / sum);
     }
     __syncthreads();
     const float* s = a.w.scores + (static_cast<size_t>(b) * a.p.H + hk * a.p.G + g0) * a.g.capr + k0 + tid;
@@ -611,7 +615,7 @@ __global__ void __launch_bounds__(kCombineThreads)
     for (int g = 0; g < gn; ++g, s += a.g.capr) {
 #pragma unroll
       for (int e = 0; e < E; ++e)
-        if (k0 + tid + e * kCombineThreads < n) acc[e] += ex2(s[e * kCombineThreads] - lse[g]);
+        if (k0 + tid + e * kCombineThreads < n) acc[e] = fmaf(ex2(s[e * kCombineThreads] - stat[g].x), stat[g].y, acc[e]);
     }
   }
   const size_t at = static_cast<size_t>(bh) * a.p.cap + k0 + tid;

@@ -517,9 +517,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t d = tb + P::kColS + t * 128;
           const uint64_t kb = k0d + static_cast<uint64_t>((t * KS + kslot) * (P::kKBytes >> 4));
 #pragma unroll
-          for (int k = 0; k < 2 * M / 16; ++k) {  // high parts, then low parts of q~
-            const int kk = k % (M / 16);
-            mma_ss(d, qa + (k * 4096 >> 4), kb + (((kk >> 2) * 16384 + (kk & 3) * 32) >> 4), kIdS, k > 0);
+          for (int k = 0; k < 2 * M / 16; ++k) {
+            // low parts of q~ first, while the sums are small, then high parts
+            const int kk = k % (M / 16), part = (k + M / 16) % (2 * M / 16);
+            mma_ss(d, qa + (part * 4096 >> 4), kb + (((kk >> 2) * 16384 + (kk & 3) * 32) >> 4), kIdS, k > 0);
           }
           // a failure-detection test withholds the first "scores ready"
           if (!(a.inject_stall && is == 0)) mma_commit(&sh.s_full[t]);

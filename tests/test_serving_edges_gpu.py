@@ -261,3 +261,37 @@ def test_readme_decode_steps():
         for h in range(Hk):
             assert names["row_pos"][b, h, :n].tolist() == list(range(first, first + n))
     assert bool(torch.isfinite(names["out"]).all())
+
+
+# ------------------------------------------------------------------ accumulated weights
+@pytest.mark.parametrize("shape", [
+    # B, H, Hk, d, m, plen: many queries, so that the errors' mean does not hang on a few of them
+    (64, 8, 8, 128, 16, 0),
+    (100, 16, 4, 200, 32, 0),
+    (64, 32, 4, 128, 32, 300),
+])
+def test_decode_weights_are_as_near_as_plain_fp32(shape):
+    """Weights of large scores: as near to 64 bits, in the mean, as fp32 arithmetic on fp32 scores."""
+    pkg = spa()
+    B, H, Hk, d, m, plen = shape
+    g = gen(B + m)
+    cap, dv, G = 48, 64, H // Hk
+    q, P = randn(g, B, H, d, dtype=BF16), (randn(g, Hk, d, m) / math.sqrt(m)).to(BF16)
+    cache = make_cache(g, B, Hk, cap, m=m, dv=dv, d=d)
+    prefix = make_cache(g, Hk, plen, m=m, dv=dv, d=d) if plen else None
+    acc = torch.zeros((B, Hk, cap), device="cuda")
+    pkg.spa_attention_decode_shared(q, P, *cache, torch.full((B,), cap, dtype=I32, device="cuda"), prefix=prefix, acc=acc)
+
+    def plain(t):
+        qt = torch.matmul(q.to(t).view(B, Hk, G, d), P.to(t)) / math.sqrt(m)
+        s = torch.matmul(qt, (cache[0].view(torch.float16).to(t) * cache[1].to(t)[..., None]).transpose(-1, -2))
+        if plen:
+            k = (prefix[0].view(torch.float16).to(t) * prefix[1].to(t)[..., None]).transpose(-1, -2)
+            s = torch.cat((s, torch.matmul(qt, k)), dim=-1)
+        e = torch.exp(s - s.amax(-1, keepdim=True))
+        return (e / e.sum(-1, keepdim=True)).sum(2)[..., :cap]
+
+    want = plain(torch.float64)
+    own, fp32 = (float((x.double() - want).norm() / want.norm()) for x in (acc, plain(torch.float32)))
+    # a quarter more at most: both round each score at its size and a probability a few times
+    assert own <= 1.25 * fp32, (own, fp32)
