@@ -48,15 +48,6 @@ __device__ __forceinline__ int row_exponent(double top) {
   return max(-125, min(125, E - 14));
 }
 
-__device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
-                                         uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-      "{%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
 __device__ __forceinline__ uint32_t pair_at(const __nv_bfloat16* x, int k, int d) {
   const uint32_t lo = k < d ? __bfloat16_as_ushort(x[k]) : 0u;
   const uint32_t hi = k + 1 < d ? __bfloat16_as_ushort(x[k + 1]) : 0u;
@@ -204,7 +195,7 @@ __global__ void __launch_bounds__(kThreads, kCtas<M>) append_kernel(const Append
 #pragma unroll
           for (int j = 0; j < M / 8; ++j) {
             const uint2 b = f[j * 32];
-            mma_bf16(c[j], a, b.x, b.y);
+            ptx::mma_bf16(c[j], a, b.x, b.y);
           }
         }
       }

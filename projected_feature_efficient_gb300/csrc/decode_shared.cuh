@@ -28,7 +28,9 @@ constexpr int kMaxCtas = 256;       // grid limit (sizes the workspace)
 constexpr int kPrefixSlots = 1024;  // prefix segments per call at most (beyond one per row tile)
 constexpr float kGrow = 40.f;       // log2 units that a running maximum may lag behind
 
-// Division of 31-bit numbers by a divisor that the host knows.
+// Division of 31-bit numbers by a divisor that the host knows: a multiplication by its
+// scaled reciprocal (Granlund and Montgomery, Division by invariant integers using
+// multiplication, 1994).
 struct FastDiv {
   uint32_t m, s;
   void set(uint32_t d) {
