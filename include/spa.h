@@ -338,7 +338,8 @@ SPA_API int spa_attention_decode(const void *q, const void *P, const void *kc, c
  *     pos       [B][N] device, or NULL: row n is at pos0 + n.
  *     table     [rot/2] device, from spa_rope_table.
  *   1 <= d <= 1024, rot even, 2 <= rot <= d.  Angles are formed without
- *   rounding modulo one turn at every position, arithmetic is fp32.
+ *   rounding modulo one turn at every position and used to 2^-48 of a turn;
+ *   arithmetic is fp32.
  * spa_rope_table (host) -- table[i] = round(inv_freq[i] / 2pi * 2^64) mod 2^64
  *   for the rot/2 frequencies f_i (host arrays; finite, else SPA_ERR_SHAPE):
  *   the advance per position in units of 2^-64 turns.
@@ -373,9 +374,9 @@ SPA_API int spa_rope(const void *q, const void *k, void *q_out, void *k_out,
  *   (bf16; H key heads here) the first count[b] (NULL: T) rows go to cache
  *   rows pos[b] .. of kc, kc_mul and vc [B][H][cap][d_v].  Rows are as
  *   spa_kcache_append writes them, up to the order of the fp32 sums; maxima
- *   next to a power of two choose their multiplier by sums in 64 bits.  For the eviction, the new rows of
- *   acc [B][H][cap] are set to 0 and those of row_pos [B][H][cap] to token[b]
- *   + t (NULL: pos[b] + t); acc and row_pos may be NULL.  No two sequences
+ *   next to a power of two choose their multiplier by sums in 64 bits.  For the
+ *   eviction, the new rows of acc [B][H][cap] are set to 0 and those of row_pos
+ *   [B][H][cap] to token[b] + t (NULL: pos[b] + t); acc and row_pos may be NULL.  No two sequences
  *   share rows, so the calls of a graph replay bit for bit.
  */
 SPA_API int spa_kcache_append_ragged(const void *k, const void *v, const void *P, void *kc,
@@ -401,7 +402,10 @@ SPA_API int spa_kcache_append_ragged(const void *k, const void *v, const void *P
  *   for rows below the length; the others are left as they are.
  *   workspace: device, 256-byte aligned, at least
  *   spa_attention_decode_shared_workspace_size bytes, overwritten, for this
- *   call alone until it has run; NULL: from the library's pool.
+ *   call alone until it has run; NULL: from the library's pool.  With weights
+ *   it holds a score of every query for every row of capacity (4 B H cap
+ *   bytes, cap to the next 128), since the lengths are known on the device
+ *   alone.
  *   Scores, softmax statistics, sums and the weights are fp32 (the projected
  *   query enters with 22 bits).  For the value product the probabilities of a
  *   sequence's own rows keep 16 bits, and those of the prefix (and of own rows

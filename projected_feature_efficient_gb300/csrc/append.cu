@@ -21,7 +21,8 @@
 // TB/s.  The 64-bit sums are dealt out over a warp's lanes, feature by feature, for the
 // columns that need them alone; with a column per lane and all features one after the
 // other a row took longer than the rest of its warp's work, and the calls 30 to 39 us.
-// 64 sequences' one row each: 6 us, two round trips to memory behind the launch.  A warp holds 16 rows' keys in registers as the A fragments, so a row
+// 64 sequences' one row each: the kernel 5.7 us, two round trips to memory behind the
+// launch (14.5 us a call, the host's time).  A warp holds 16 rows' keys in registers as the A fragments, so a row
 // needs one load and no staging; value rows are copied by CTAs of their own, whose
 // loads wait for nothing else.  With P_h staged element by element and the values
 // behind the keys in the same warps the prompts took 33 us.

@@ -168,8 +168,9 @@ __global__ void __launch_bounds__(kQueryThreads) decode_query_kernel(const __gri
 // cache bounds the kernel, and the products are a fifth of the time that the bytes take.  (The same rows on
 // tcgen05, 128 rows for a group of 4, took 4 times as long: each short segment
 // drains the scores, the sums and their output in turn.)
-// 128 sequences of 0 to 2047 rows, 8 key heads (m = 64, d_v = 128): 77 us, 412 MB read
-// at 5.4 TB/s; 16 sequences of 17 to 8191 rows, 4 key heads (m = 32): 17 us for 85 MB.
+// 128 sequences of 0 to 2047 rows, 8 key heads (m = 64, d_v = 128): 78 us, 412 MB read
+// at 5.3 TB/s; 16 sequences of 17 to 8191 rows, 4 key heads (m = 32): 18 us for 85 MB;
+// one sequence of 131072 rows, 8 key heads (m = 32): 80 us for the call, 340 MB.
 // Behind a prefix kernel it waits for that one's end (moving in as its CTAs left took 47
 // us for 50 with 32768 shared keys and 255 for 262 with 65536, but read the queries and
 // offsets without the wait that makes another kernel's results visible).  With SMs of
@@ -497,7 +498,7 @@ __device__ __forceinline__ float2 stats_of(const Params& a, const Parts& x, int 
 }
 
 // Bound by the latency of a row's chain (lengths, statistics, sums) where there are few
-// rows, and by issued instructions with weights: 7 us for 1024 rows of 19 + 1 parts, 24
+// rows, and by issued instructions with weights: 7 us for 1024 rows of 19 + 1 parts, 23
 // us for 4096 rows and 4.2 million weights (45 MB read).  One, two or eight warps per
 // row: 13, 7 and 8 us, and 23, 26 and 32 us.
 // Four warps per row of the output (the first `oblocks` blocks), each a quarter

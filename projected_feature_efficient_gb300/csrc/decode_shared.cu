@@ -42,7 +42,7 @@
 // for 0.0017 with the output's alone); their sums, and the weights that are
 // accumulated, take them in fp32.  With the parts that bf16 leaves as a second value
 // product, as the kernel of the own rows has it, 65536 keys for 512 rows of 8 key
-// heads took 323 us for 250 in the whole call and 32768 keys for 128 rows 55 for 46:
+// heads took 323 us for 251 in the whole call and 32768 keys for 128 rows 55 for 46:
 // the tensor pipe and the softmax are what bounds this kernel, so one part it is.
 //
 // Softmax in base 2 with the running maximum moved only when a row's tile sum
@@ -53,16 +53,17 @@
 // never meet another's rows.
 //
 // What bounds it.  65536 keys against 512 rows of each of 8 key heads (m = 64, d_v =
-// 128): 148 us, 2450 cycles per tile and row tile; the products alone would take 1070
+// 128): 155 us, 2570 cycles per tile and row tile; the products alone would take 1070
 // (the score product's K is 2 m for the two parts of q~).  A tile moves 176 KB through
 // the SM's shared memory, 1400 cycles at 128 bytes a cycle: both operands of the score
 // product, V, what TMA writes and the range pass.  The issuer is held up by the tensor
-// pipe for 1600 cycles of a tile and waits for probabilities for 630.  32768 keys
-// against 128 rows (m = 32): 28 us, 1750 cycles per tile, which is the memory
-// bandwidth, and 10000 + 6000 cycles of start and end.  One score buffer that both
+// pipe for 1600 cycles of a tile and waits for probabilities for 630 (clocks of a build
+// without the check of a tile's range, whose tiles took 2450).  32768 keys against 128
+// rows (m = 32): 29.5 us, 1750 cycles per tile, which is the memory bandwidth, and
+// 10000 + 6000 cycles of start and end.  One score buffer that both
 // streams read into registers, with the probabilities beside it and the scores three
 // tiles ahead, took the softmax out of the way between two score products, and the
-// large case took 266 us for 251: the issuer then waited for nothing, and each product
+// large case took 266 us for 251 then: the issuer then waited for nothing, and each product
 // took longer.
 //
 // Every wait is bounded; a role that gives up sets the CTA's abort flag and
@@ -838,7 +839,9 @@ Geo geometry(const DecodeSharedParams& p, int sms) {
   // the split of the prefix with the shortest schedule, in cycles: rounds of segments,
   // each its tiles and about two tiles' time of start and end, and the partial sums'
   // way to memory and back (65536 keys for 512 rows of 8 key heads: 4, 9, 14, 19, 28
-  // segments per row tile 258, 251, 256, 259, 270 us for the whole call)
+  // segments per row tile 258, 251, 256, 259, 270 us for the whole call, of a build that
+  // takes 262 now).  Cycles per tile were measured for m = 32 and 64 with d_v = 128; the
+  // one for m = 128 is an estimate.
   if (g.PT > 0) {
     const long long tile = p.m <= 32 ? 1750 : p.m == 64 ? 2400 : 3500;
     const long long sums = rowtiles * g.rows * p.dv * 8 / 3500;

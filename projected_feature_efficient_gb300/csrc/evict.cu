@@ -19,12 +19,13 @@
 //                        to move, a lane per row
 //   evict_move_kernel    the rows' K~, multiplier and V, a warp per row; many warps
 //                        with a row each in flight beat fewer with more (64 pairs
-//                        of up to 16383 rows, caches flushed: 52 us for the whole
-//                        call, two rows 54, four 60, eight 71)
+//                        of up to 16383 rows: 52 us for a call with the caches
+//                        flushed before it, two rows 54, four 60, eight 71)
 // The first is bound by issued instructions and the latency of its passes, the second
 // by memory.  Dropping one of 2049 rows of 512 pairs: selection 9.5 us, move 4.7 us
 // (what it cannot do without: 3.1 us of memory traffic); 4096 of up to 16383 rows of
-// 64 pairs, which occupy 64 SMs in the selection: 46 us in all (traffic: 13.8 us).
+// 64 pairs, which occupy 64 SMs in the selection: 46.7 us a call in a stream of calls,
+// selection 26 us, move 15 to 17 us (traffic: 13.8 us).
 // Selections that were measured on 512 pairs of 2049 rows: a histogram of 8 bits per
 // pass 18 us, equal digits of a warp counted by one lane 39 us, two bits per pass by
 // counting keys above three candidates 31 us, the worst row looked for 9.5 us.

@@ -17,8 +17,8 @@
 // same vector of pairs in several heads of one token, so the sines are formed
 // once per thread and used for each of them, four heads' loads in flight.
 // 2 x 8192 rows of 20 heads of 128 bf16 features: 29 us, 5.7 TB/s (24.8 us at the
-// measured 6.8 TB/s); 8191 rows of 15 heads of 96 fp32 features: 4.6 TB/s with the
-// launch.  With a head at a time and the pairs converted one by one the first took
+// measured 6.8 TB/s); 8191 rows of 16 heads of 96 fp32 features: 20.6 us a call, 4.9
+// TB/s with the launch (the kernel 15.4 us).  With a head at a time and the pairs converted one by one the first took
 // 45 us.
 #include "kernels.cuh"
 
