@@ -128,6 +128,25 @@ def test_decode_keys_of_other_magnitudes_in_a_tile(m, own, kind):
     check_exact(pkg, q, P, cache, lens, prefix)
 
 
+@pytest.mark.parametrize("m", [16, 64, 128])
+def test_decode_many_tiles_with_and_without_one_range(m):
+    """Some twenty tiles one behind the other on every SM, at random with a row of zeros or without:
+    each key's weight is that of its own multiplier."""
+    pkg = spa()
+    g = gen(110 + m)
+    B, H, Hk, d, dv, n = 1, 40, 1, 64, 64, 400000
+    q = (randn(g, B, H, d) * 2.0 ** 14).to(BF16)
+    P = (randn(g, Hk, d, m) / math.sqrt(m)).to(BF16)
+    x = torch.randn((Hk, n, m), generator=g, device="cuda", dtype=torch.float64) * math.sqrt(d / m) * 2.0 ** -14
+    x *= torch.exp2(-torch.randint(0, 3, (Hk, n, 1), generator=g, device="cuda").double())
+    wide = torch.nonzero(torch.rand(n // 128, generator=g, device="cuda") < 0.5)[:, 0]
+    x[:, wide * 128 + torch.randint(0, 128, wide.shape, generator=g, device="cuda")] = 0
+    kc, mul = rows_of(x)
+    del x
+    check_exact(pkg, q, P, (kc[None], mul[None], randn(g, B, Hk, n, dv, dtype=BF16)),
+                torch.tensor([n - 5], dtype=I32, device="cuda"))
+
+
 @pytest.mark.parametrize("own", [False, True])
 @pytest.mark.parametrize("m", [16, 64, 128])
 def test_decode_scores_that_grow_along_the_keys(m, own):
