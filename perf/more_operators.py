@@ -1,7 +1,5 @@
 """Operators around the projected attention, in plain form and as the library computes them.
 
-  window    the projected attention of a whole sequence where a query sees its newest keys and a few first keys
-            that stay visible, query heads in groups on shared key heads; forward, or forward and gradients
   norm      norms of queries and keys for each head with the rotary positions in the same pass, and the gradient
   pack      full blocks of 64 rows of the 16-bit projected cache become pages of 8-bit values with one scale per
             block and head; the rows behind them move to the front
@@ -30,6 +28,9 @@ def listed():
         # a prompt chunk as the fused q/k/v product leaves it (token-major), half of each head rotated
         dict(name="norm prompt", op="norm", B=2, H=16, G=4, N=8192, d=128, rot=64, interleaved=True, far=8192,
              gradient=False, dtype="bf16"),
+        # fp32 at an odd length and an odd head width
+        dict(name="norm odd", op="norm", B=1, H=12, G=3, N=8191, d=96, rot=96, interleaved=False, far=262144,
+             gradient=False, dtype="f32"),
         # the gradients of a training step's queries, keys and weights
         dict(name="norm gradient", op="norm", B=4, H=16, G=4, N=8192, d=128, rot=128, interleaved=False, far=8192,
              gradient=True, dtype="bf16"),
@@ -44,18 +45,15 @@ def listed():
         dict(name="decode small", op="decode", B=1, H=8, G=1, d=64, m=16, dv=64, lo=300, hi=300, window=0, sink=0),
         # a batch of ragged sequences
         dict(name="decode batch", op="decode", B=64, H=32, G=4, d=128, m=32, dv=128, lo=17, hi=8191, window=0, sink=0),
+        # two very long sequences
+        dict(name="decode long", op="decode", B=2, H=64, G=8, d=128, m=64, dv=128, lo=131071, hi=131072, window=0,
+             sink=0),
         # long sequences that see their newest 4096 keys and the first few; pages in between are gone
         dict(name="decode window", op="decode", B=32, H=16, G=2, d=128, m=32, dv=128, lo=3000, hi=65536, window=4096,
              sink=4),
-        # prompts under a sliding window, 16 query heads on 4 key heads
-        dict(name="window prompt", op="window", B=2, H=16, G=4, N=8192, d=128, m=32, dv=128, window=1024, sink=4,
-             gradient=False),
-        # a training step of the same
-        dict(name="window gradient", op="window", B=1, H=16, G=4, N=8192, d=128, m=32, dv=128, window=1024, sink=4,
-             gradient=True),
-        # a small ragged training step, first keys of more than a tile
-        dict(name="window gradient odd", op="window", B=3, H=6, G=3, N=1021, d=64, m=64, dv=64, window=300, sink=130,
-             gradient=True),
+        # many query heads on each key head
+        dict(name="decode wide", op="decode", B=16, H=64, G=16, d=128, m=32, dv=128, lo=1023, hi=16383, window=0,
+             sink=0),
     ]
 
 
@@ -64,7 +62,7 @@ def _log(rng, lo, hi):
 
 
 def draw(rng):
-    op = rng.choice(["norm", "norm", "pack", "decode", "decode", "window", "window"])
+    op = rng.choice(["norm", "norm", "pack", "decode", "decode"])
     if op == "norm":
         G = rng.choice([1, 2, 4])
         H = G * rng.choice([1, 2, 3, 4, 8])
@@ -75,15 +73,6 @@ def draw(rng):
         B = _log(rng, 1, max(1, min(64, most // N)))
         return dict(op=op, B=B, H=H, G=G, N=N, d=d, rot=2 * rng.randint(1, d // 2), interleaved=rng.random() < 0.5,
                     far=_log(rng, N + 1, 1 << 20), gradient=rng.random() < 0.5, dtype=dtype)
-    if op == "window":
-        G = rng.choice([1, 2, 3, 4, 8])
-        H = G * rng.choice([1, 2, 4])
-        N = _log(rng, 1, 8192)
-        B = _log(rng, 1, max(1, min(16, (1 << 30) // (H * N * N))))
-        window = rng.choice([0, _log(rng, 1, N), _log(rng, 1, N), min(N, 1024)])
-        return dict(op=op, B=B, H=H, G=G, N=N, d=rng.choice([64, 128]), m=rng.choice([16, 32, 64]),
-                    dv=rng.choice([64, 128]), window=window, sink=rng.choice([0, 1, 4, 130]) if window else 0,
-                    gradient=rng.random() < 0.5)
     m = rng.choice([16, 32, 32, 64, 128])
     dv = rng.choice([64, 128])
     if op == "pack":
@@ -113,12 +102,6 @@ def _generator(seed):
 
 def _normal(g, *shape, dtype=torch.float32):
     return torch.randn(shape, generator=g, device="cuda").to(dtype)
-
-
-def _rows(g, *shape):
-    """Rows of norm sqrt(d), as a norm leaves them, in bf16."""
-    x = torch.randn(shape, generator=g, device="cuda")
-    return (x * (math.sqrt(shape[-1]) / x.norm(dim=-1, keepdim=True))).to(torch.bfloat16)
 
 
 def _key_rows(g, *shape, d):
@@ -173,17 +156,6 @@ def prepare(case, seed):
         else:
             s["q_out"] = torch.empty((B, H, N, d), dtype=dt, device="cuda")
             s["k_out"] = torch.empty((B, Hk, N, d), dtype=dt, device="cuda")
-    elif c["op"] == "window":
-        B, H, N, d, dv = c["B"], c["H"], c["N"], c["d"], c["dv"]
-        Hk = H // c["G"]
-        s["q"], s["k"] = _rows(g, B, H, N, d), _rows(g, B, Hk, N, d)
-        s["v"] = _normal(g, B, Hk, N, dv, dtype=torch.bfloat16)
-        s["P"] = (torch.randn((Hk, d, c["m"]), generator=g, device="cuda") / math.sqrt(c["m"])).to(torch.bfloat16)
-        s["out"] = torch.empty((B, H, N, dv), dtype=torch.bfloat16, device="cuda")
-        if c["gradient"]:
-            s["dO"] = _normal(g, B, H, N, dv, dtype=torch.bfloat16)
-            s["lse"] = torch.empty((B, H, N), dtype=torch.float32, device="cuda")
-            s["grads"] = [torch.empty_like(s[x]) for x in ("q", "k", "v", "P")]
     elif c["op"] == "pack":
         B, H, m, dv, cap = c["B"], c["H"], c["m"], c["dv"], c["cap"]
         s["kc"], s["mul"] = _key_rows(g, B, H, cap, m, d=128)
@@ -262,35 +234,6 @@ def _plain_norm(s):
     dq, dwq = gradient(s["q"], s["wq"], s["dq_out"])
     dk, dwk = gradient(s["k"], s["wk"], s["dk_out"])
     return dq, dk, dwq, dwk
-
-
-def _plain_window(s):
-    c = s["case"]
-    B, H, G, N, m = c["B"], c["H"], c["G"], c["N"], c["m"]
-    Hk = H // G
-    P, k, v = s["P"].float(), s["k"].float(), s["v"].float()
-    q = s["q"].float().view(B, Hk, G * N, c["d"])
-    qp, kp = torch.matmul(q, P), torch.matmul(k, P)
-    i, j = torch.arange(N, device="cuda")[:, None], torch.arange(N, device="cuda")
-    seen = j <= i
-    if c["window"]:
-        seen &= (j > i - c["window"]) | (j < c["sink"])
-    scores = (torch.matmul(qp, kp.transpose(-1, -2)) / math.sqrt(m)).view(B, Hk, G, N, N).masked_fill(~seen, -math.inf)
-    e = torch.exp(scores - scores.amax(dim=-1, keepdim=True))
-    e = (e / e.sum(dim=-1, keepdim=True)).view(B, Hk, G * N, N)
-    del scores
-    out = torch.matmul(e, v)
-    if not c["gradient"]:
-        return out.view(B, H, N, -1).to(torch.bfloat16)
-    dO = s["dO"].float().view(B, Hk, G * N, c["dv"])
-    dv = torch.matmul(e.transpose(-1, -2), dO)
-    ds = torch.matmul(dO, v.transpose(-1, -2))
-    ds = e * (ds - (dO * out).sum(dim=-1, keepdim=True)) / math.sqrt(m)
-    dqp, dkp = torch.matmul(ds, kp), torch.matmul(ds.transpose(-1, -2), qp)
-    dq, dk = torch.matmul(dqp, P.transpose(-1, -2)), torch.matmul(dkp, P.transpose(-1, -2))
-    dP = (torch.matmul(q.transpose(-1, -2), dqp) + torch.matmul(k.transpose(-1, -2), dkp)).sum(dim=0)
-    found = out.view(B, H, N, -1), dq.view(B, H, N, -1), dk, dv, dP
-    return tuple(x.to(torch.bfloat16) for x in found)
 
 
 def _value_order():
@@ -383,15 +326,6 @@ def _own(s):
     if c["op"] == "norm":
         return spa.spa_norm_rope(s["q"], s["wq"], s["table"], s["pos"], k=s["k"], wk=s["wk"], eps=EPS,
                                  interleaved=c["interleaved"], out=s["q_out"], k_out=s["k_out"])
-    if c["op"] == "window":
-        args = s["q"], s["k"], s["v"], s["P"]
-        if not c["gradient"]:
-            return spa.spa_attention_window_fwd(*args, window=c["window"], sink=c["sink"], out=s["out"])
-        low = torch.empty_like(s["out"])  # what the output's rounding left, for the gradient
-        out = spa.spa_attention_window_fwd(*args, window=c["window"], sink=c["sink"], out=s["out"], out_lo=low,
-                                           lse=s["lse"])
-        return out, *spa.spa_attention_window_bwd(*args, out, low, s["lse"], s["dO"], window=c["window"],
-                                                  sink=c["sink"], grads=s["grads"])
     if c["op"] == "pack":
         spa.spa_kcache8_pack(s["kc"], s["mul"], s["vc"], s["len"], (s["kc8"], s["ks"], s["vc8"], s["vs"]), s["table"],
                              s["blocks"], lens_out=s["len_out"], blocks_out=s["blocks_out"])
@@ -402,7 +336,7 @@ def _own(s):
                                      out=s["out"])
 
 
-_PLAIN = dict(window=_plain_window, norm=_plain_norm, pack=_plain_pack, decode=_plain_decode)
+_PLAIN = dict(norm=_plain_norm, pack=_plain_pack, decode=_plain_decode)
 
 
 def run(state):
@@ -419,17 +353,6 @@ def work(case):
         moved = (3 if c["gradient"] else 2) * n * c["d"] * size
         return dict(bytes=moved + 4 * c["B"] * c["N"] + 4 * c["rot"] + 2 * size * c["d"] + (8 * c["d"] if c["gradient"] else 0),
                     flops=n * ((11 if c["gradient"] else 4) * c["d"] + 3 * c["rot"]))
-    if c["op"] == "window":
-        B, H, N, d, m, dv, w = c["B"], c["H"], c["N"], c["d"], c["m"], c["dv"], c["window"]
-        Hk = H // c["G"]
-        pairs = B * H * sum(i + 1 if not w or i < w else w + min(c["sink"], i + 1 - w) for i in range(N))
-        rows, proj = B * N * (H + Hk) * d, 2 * B * N * (H + Hk) * d * m
-        values = B * N * (H + Hk) * dv  # v and the output
-        if not c["gradient"]:
-            return dict(bytes=2 * (rows + values + Hk * d * m), flops=2 * pairs * (m + dv) + proj)
-        # the inputs, the upstream gradient, the output, and a gradient for each input
-        return dict(bytes=2 * (2 * rows + 2 * values + 2 * Hk * d * m),
-                    flops=2 * pairs * (m + dv) + proj + 2 * pairs * (3 * m + 2 * dv) + 2 * proj)
     lens = _lengths(c["lo"], c["hi"], c["B"])
     if c["op"] == "pack":
         rows = c["H"] * sum(BLOCK * (n // BLOCK) for n in lens)
@@ -474,34 +397,6 @@ def exact(case, seed):
             weight = s["w" + name].double().requires_grad_()
             found.append(torch.autograd.grad(apply(x, weight), (x, weight), s["d%s_out" % name].double()))
         return found[0][0], found[1][0], found[0][1], found[1][1]
-    if c["op"] == "window":
-        B, H, G, N, d, m, dv = (c[x] for x in ("B", "H", "G", "N", "d", "m", "dv"))
-        if B * H * N * N * (5 if c["gradient"] else 2) > 1e10:
-            return None
-        new = lambda *shape: torch.zeros(shape, dtype=torch.float64, device="cuda")  # noqa: E731
-        out, dq = new(B, H, N, dv), new(B, H, N, d)
-        dk, dvv, dP = new(B, H // G, N, d), new(B, H // G, N, dv), new(H // G, d, m)
-        row = torch.arange(N, device="cuda")
-        for b in range(B):
-            for h in range(H):
-                P, k, v = s["P"][h // G].double(), s["k"][b, h // G].double(), s["v"][b, h // G].double()
-                kp = k @ P
-                for r0 in range(0, N, 2048):
-                    cut = slice(r0, r0 + 2048)
-                    q, i = s["q"][b, h, cut].double(), row[cut, None]
-                    far = (i - row >= c["window"]) & (row >= c["sink"]) if c["window"] else torch.zeros_like(i, dtype=torch.bool)
-                    a = torch.softmax((q @ P @ kp.T / math.sqrt(m)).masked_fill((row > i) | far, -math.inf), dim=-1)
-                    out[b, h, cut] = a @ v
-                    if c["gradient"]:
-                        g = s["dO"][b, h, cut].double()
-                        dvv[b, h // G] += a.T @ g
-                        ga = g @ v.T
-                        gs = a * (ga - (a * ga).sum(dim=-1, keepdim=True)) / math.sqrt(m)
-                        gq, gk = gs @ kp, gs.T @ (q @ P)
-                        dq[b, h, cut] = gq @ P.T
-                        dk[b, h // G] += gk @ P.T
-                        dP[h // G] += q.T @ gq + k.T @ gk
-        return (out, dq, dk, dvv, dP) if c["gradient"] else out
     if c["op"] == "pack":
         kc8, vc8 = torch.zeros(s["kc8"].shape, dtype=torch.float64, device="cuda"), torch.zeros(
             s["vc8"].shape, dtype=torch.float64, device="cuda")
