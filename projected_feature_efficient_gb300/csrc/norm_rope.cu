@@ -293,7 +293,13 @@ __global__ void __launch_bounds__(kThreads, kFwdBlocks<UPL, INTER>) norm_rope_ke
   const T* x = static_cast<const T*>(p.x[t]) + b * p.xs[t][0] + n * p.xs[t][2] + h0 * xs;
   T* y = static_cast<T*>(p.y[t]) + b * p.ys[t][0] + n * p.ys[t][2] + h0 * ys;
   R row[E];
+  // Places that no load fills hold what the row before left there, where a NaN is one in every
+  // place: they are 0 again before each row, or the next row's sum would take them in.
   auto fetch = [&](int left) {
+    if constexpr (!EXACT) {
+#pragma unroll
+      for (int e = 0; e < E; ++e) row[e].clear();
+    }
     if (left >= E) {
 #pragma unroll
       for (int e = 0; e < E; ++e, x += xs) pl.read(x, row[e]);
@@ -304,7 +310,7 @@ __global__ void __launch_bounds__(kThreads, kFwdBlocks<UPL, INTER>) norm_rope_ke
     }
   };
 #pragma unroll
-  for (int e = 0; e < E; ++e) row[e].clear();  // what no load fills stays 0
+  for (int e = 0; e < E; ++e) row[e].clear();
   fetch(rows);
   // y_a = r (a ca - b sb), y_b = r (a sa + b cb): weights and turn in one
   using D = Twos<UPL, PR>;

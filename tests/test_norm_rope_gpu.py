@@ -302,3 +302,43 @@ def test_training_step(causal):
     # bf16 are off by 2^-8, a logit of up to about 30 by 0.1 where one feature carries it: 5e-2 in all
     for got, want in zip((dq, dk, dwq, dwk), ref):
         assert float((got.double() - want).norm() / want.norm()) < 5e-2
+
+
+def odd_rows(x):
+    """x with rows whose addresses no vector fits: one feature between them."""
+    B, H, N, d = x.shape
+    y = torch.empty(B, H, N, d + 1, dtype=x.dtype, device="cuda")[..., :d]
+    return y.copy_(x)
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("d, odd", [(96, False), (80, False), (200, False), (33, False), (96, True), (128, False)])
+def test_a_row_that_is_not_finite_stays_alone(d, odd, dtype, interleaved):
+    """NaN and infinities in one head's row reach no other row, forward or backward: the others keep their bits."""
+    B, H, Hk, N, rot = 2, 9, 8, 10007, 32
+    g = gen(d + odd)
+    pkg = spa()
+    table = pkg.rope_table(pkg.rope_frequencies(rot))
+    q, k = (randn(g, B, h, N, d, dtype=dtype) for h in (H, Hk))
+    dq_out, dk_out = randn(g, B, H, N, d, dtype=dtype), randn(g, B, Hk, N, d, dtype=dtype)
+    w = (1 + 0.3 * randn(g, d)).to(dtype)
+    bad = [(0, 0, 0), (1, 2, N - 1), (0, 1, 77), (1, 5, 4096)]  # (sequence, head, token)
+    values = (math.nan, math.inf, -math.inf, math.nan)
+
+    def calls(q, k):
+        if odd:
+            q, k = odd_rows(q), odd_rows(k)
+        return (*pkg.spa_norm_rope(q, w, table, k=k, wk=w, interleaved=interleaved),
+                *pkg.spa_norm_rope_bwd(dq_out, q, w, table, dk_out=dk_out, k=k, wk=w, interleaved=interleaved)[:2])
+
+    want = calls(q, k)
+    for (b, h, n), x in zip(bad, values):
+        for t in (q, k):
+            t[b, h, n, 3] = x
+    got = calls(q, k)
+    for x, y in zip(got, want):
+        for b, h, n in bad:
+            assert bool(x[b, h, n].isnan().any())
+            x[b, h, n] = y[b, h, n] = 0
+        assert torch.equal(x, y)
