@@ -463,26 +463,35 @@ __device__ __forceinline__ void page_unit(const Decode8Params& p, const Place& a
       }
     }
   });
+  float f[NT][2];  // of a score
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) f[t][e] = scale.x * x.qm[t][e];
   const int key0 = at.block() * kPageRows;
   if (key0 < at.s.lo && key0 + kPageRows > p.sink) {  // a page that the window's or the first keys' border cuts
+    // scaled before they are masked: a factor may be 0, which would make a NaN of the masked score
 #pragma unroll
     for (int j = 0; j < 4; ++j)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int key = key0 + 16 * j + 8 * e + r;
-        if (key < at.s.lo && key >= p.sink)
+        const bool seen = key >= at.s.lo || key < p.sink;
 #pragma unroll
-          for (int t = 0; t < NT; ++t) s[t][j][2 * e] = s[t][j][2 * e + 1] = -INFINITY;
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) s[t][j][2 * e + i] = seen ? s[t][j][2 * e + i] * f[t][i] : -INFINITY;
       }
+#pragma unroll
+    for (int t = 0; t < NT; ++t) f[t][0] = f[t][1] = 1.f;
   }
   // the value scale's exponent: the products below stay under 2^(kGrow + 1)
   const float shift = static_cast<float>((__float_as_int(scale.y) >> 23 & 255) - 127);
-  float f[NT][2], top[NT][2];
+  float top[NT][2];
 #pragma unroll
   for (int t = 0; t < NT; ++t)
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      f[t][e] = scale.x * x.qm[t][e];
       float most = s[t][0][e];
 #pragma unroll
       for (int j = 0; j < 4; ++j) most = max3(most, s[t][j][e], s[t][j][2 + e]);

@@ -490,3 +490,21 @@ def test_serving_loop_and_graph():
         graph.replay()
         assert torch.equal(other, outs[t])
     assert all(torch.equal(a, b) for a, b in zip(again[2:], state[2:]))
+
+
+@pytest.mark.parametrize("G", [3, 11])
+def test_decode_small_scores_on_a_border(G):
+    """Pages of zero keys, whose scale is the smallest, under queries so small that scale times query is nothing: the
+    keys that a border hides stay hidden, the others weigh the same."""
+    pkg = spa()
+    g = gen(41 + G)
+    d, m, dv, lens = 64, 32, 64, [300, 230, 129]
+    pages, table, blocks, left = pool(g, pkg, lens, 1, m, dv)
+    bytes_of(pages[0]).zero_()
+    pages[1].fill_(2.0 ** -100)
+    kc, mul, vc = open_rows(g, 3, 1, 64, m, dv)
+    q = (randn(g, 3, G, d) * 2.0 ** -60).to(BF16)
+    P = (randn(g, 1, d, m) / math.sqrt(m)).to(BF16)
+    for window, sink in ((100, 0), (100, 7), (150, 70)):
+        got = pkg.spa_attention_decode8(q, P, pages, table, blocks, kc, mul, vc, left, window=window, sink=sink)
+        check_decode(got, *decode_reference(q, P, pages, table, blocks, kc, mul, vc, left, window, sink))
