@@ -481,7 +481,8 @@ SPA_API int spa_kcache_evict(void *kc, float *kc_mul, void *v, const float *acc,
  * query whose tile of 128 keys it lies in.
  *   SPA_BF16 only, d in {64, 128}, m in {16, 32, 64}, d_v in {64, 128}
  *   (SPA_ERR_UNSUPPORTED); H a multiple of Hk, B*H <= 65535, N <= 2^30, window,
- *   sink >= 0; 16-byte aligned pointers, lse 4-byte.  Without rows dP is zeroed.
+ *   sink >= 0; 16-byte aligned pointers, lse 4-byte.  Without queries dk, dv and dP
+ *   are zeroed.
  *   workspace: device, 256-byte aligned, at least
  *   spa_attention_window_workspace_size bytes (gradient != 0: the backward's),
  *   overwritten, for this call alone until it has run; NULL: from the library's

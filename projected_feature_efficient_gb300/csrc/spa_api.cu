@@ -1616,9 +1616,13 @@ int spa_attention_window_bwd(const void* q, const void* k, const void* v, const 
                              size_t workspace_bytes, void* stream) {
   int st = check_window(B, H, Hk, N, d, m, d_v, window, sink, dtype);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (st == kEmpty) {  // a sum over no rows
-    const size_t n = d > 0 && m > 0 ? static_cast<size_t>(Hk) * d * m : 0;
-    return dP && n ? cuda_status(cudaMemsetAsync(dP, 0, n * 2, s)) : SPA_OK;
+  if (st == kEmpty) {  // sums over no queries; H = 0 leaves keys
+    const size_t keys = static_cast<size_t>(B) * Hk * N, n = static_cast<size_t>(Hk) * d * m;
+    if ((keys * d && !dk) || (keys * d_v && !dv)) return SPA_ERR_NULL;
+    if (dP && n && (st = cuda_status(cudaMemsetAsync(dP, 0, n * 2, s))) != SPA_OK) return st;
+    if (keys * d && (st = cuda_status(cudaMemsetAsync(dk, 0, keys * d * 2, s))) != SPA_OK) return st;
+    if (keys * d_v && (st = cuda_status(cudaMemsetAsync(dv, 0, keys * d_v * 2, s))) != SPA_OK) return st;
+    return SPA_OK;
   }
   if (st) return st;
   if ((st = check_forward_ptrs(q, k, v, P, out))) return st;

@@ -378,3 +378,15 @@ def test_two_calls_at_once():
                 assert all(torch.equal(a, b) for a, b in zip(one[:3], ref[:3]))
                 for a, b in zip(one[3:], ref[3:]):  # fp32 sums in another order, before one rounding to bf16
                     assert float((a.double() - b.double()).norm() / b.double().norm()) <= 2.0 ** -8
+
+
+def test_key_heads_without_queries():
+    """No query head on two key heads: their gradients are zero, and are written."""
+    pkg = spa()
+    q, k, v, P, dO = inputs(2, 0, 2, 130, 64, 32, 128)
+    out, lo = (torch.empty(2, 0, 130, 128, dtype=BF16, device="cuda") for _ in range(2))
+    lse = torch.empty(2, 0, 130, device="cuda")
+    grads = [torch.full_like(t, math.nan) for t in (q, k, v, P)]
+    got = pkg.spa_attention_window_bwd(q, k, v, P, out, lo, lse, dO, window=9, sink=1, grads=grads)
+    assert [t.shape for t in got] == [t.shape for t in (q, k, v, P)]
+    assert not any(bool(t.any()) for t in got)  # NaN counts as true
