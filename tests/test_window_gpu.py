@@ -390,3 +390,28 @@ def test_key_heads_without_queries():
     got = pkg.spa_attention_window_bwd(q, k, v, P, out, lo, lse, dO, window=9, sink=1, grads=grads)
     assert [t.shape for t in got] == [t.shape for t in (q, k, v, P)]
     assert not any(bool(t.any()) for t in got)  # NaN counts as true
+
+
+@pytest.mark.parametrize("case", CASES)
+def test_log_sum_exp_of_each_row(case):
+    """Each row's log-sum-exp against a bound of its own terms."""
+    B, H, Hk, N, d, m, dv, window, sink = case
+    pkg = spa()
+    q, k, v, P, _ = inputs(B, H, Hk, N, d, m, dv)
+    lse, lo = torch.empty(B, H, N, device="cuda"), torch.empty(B, H, N, dv, dtype=BF16, device="cuda")
+    pkg.spa_attention_window_fwd(q, k, v, P, window=window, sink=sink, out_lo=lo, lse=lse)
+    x, y, p = q.double().view(B, Hk, H // Hk, N, d), k.double()[:, :, None], P.double()[:, None]
+    root, see = math.sqrt(m), seen(N, window, min(sink, N))
+    dot = lambda a, b: (a @ b.transpose(-1, -2) / root).masked_fill(~see, -math.inf)  # noqa: E731
+    s = dot(x @ p, y @ p)
+    # A logit: both operands rounded to fp16 (or to three bf16 parts), 2^-11 of a term each; the projections' sums of
+    # d products in fp32 and the logit's of m, with ten roundings of scales and exponents, 2^-24 each of the largest
+    # that the magnitudes give.  The log-sum-exp is off by no more than a logit of the row; the weights in its sum are
+    # rounded to bf16, half a step 2^-8 of each, and a sum of N and the logarithm add N + 8 roundings.
+    terms = dot((x @ p).abs(), (y @ p).abs()).amax(-1)
+    sizes = dot(x.abs() @ p.abs(), y.abs() @ p.abs()).amax(-1)
+    tol = 2.0 ** -10 * terms + (2 * d + m + 10) * 2.0 ** -24 * sizes + 2.0 ** -8 + (N + 8) * 2.0 ** -24
+    ref = torch.logsumexp(s, -1)
+    tol = tol + 2.0 ** -23 * ref.abs()
+    over = ((lse.double().view(ref.shape) - ref).abs() - tol).max()
+    assert float(over) <= 0, float(over)
