@@ -583,9 +583,11 @@ SPA_API int spa_norm_rope_bwd(const void *q, const void *k, const void *wq, cons
  *   lens[b] and masked open rows may hold anything, infinities and NaN included.
  *   cap = 0: no open rows (NULL), width = 0: no pages (NULL).
  *   Scores, statistics and sums are fp32; the projected query enters with 22
- *   bits, the probabilities are rounded to fp16 for pages and to 16 bits for open
- *   rows, both products take K~ and V as they are stored.  Results do not depend
- *   on the order in which warps run.  Scales need not be powers of two.
+ *   bits, the probabilities of a page are rounded to fp16 against its largest one
+ *   (11 bits of all down to 2^-26 of it), those of open rows to 16 bits, both
+ *   products take K~ and V as they are stored.  Sums of weighted values come
+ *   before the division: 2^8 n max|V| must lie in the range of fp32.  Results do
+ *   not depend on the order in which warps run.  Scales need not be powers of two.
  *   workspace: as above, spa_attention_decode8_workspace_size bytes.
  *   SPA_BF16 only; 1 <= d <= 256, m in {16, 32, 64, 128}, d_v in {64, 128}, H a
  *   multiple of Hk, B*H <= 65535, 64 width + cap < 2^31, window, sink >= 0.

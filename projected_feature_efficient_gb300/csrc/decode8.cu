@@ -12,13 +12,15 @@
 //   decode8_combine_kernel  the parts of a row joined
 //
 // e4m3 values are exact in fp16, so both products run on them unscaled in fp16 with fp32
-// sums, the scales taken outside: the key scale multiplies the scores, and the value scale
-// the probabilities, in fp32.  The running maximum M of a head follows s + log2 of the value
-// scale's power of two, so that these products stay below 2^(kGrow + 1) and nothing depends
-// on how large the values are; the sum of probabilities is relative to the same M.  For the
-// value product they are rounded to fp16, 2^-12 of a term, where the output's own rounding
-// is 2^-9: two parts would be half as many conversions again and change the fourth digit of
-// the error.
+// sums, the scales taken outside, in fp32: the key scale multiplies the scores, the value
+// scale a page's sums.  A page's weights are held against the page's own maximum, 2^kTop at
+// the largest, and rounded to fp16: 2^-12 of a weight for all down to 2^-(kTop + 14) of it,
+// 2^-(kTop + 25) of the largest below that.  The page's sums of weights and of weighted values
+// then join the running ones in fp32 by one factor.  (Against the running maximum, weights
+// 2^14 below it lost bits and 2^25 below it all, but not in the sum of weights: where a first
+// key of value zero lies 16 nats above 8192 others, a tenth of the output.  Two fp16 parts, 22
+// bits: 16 sequences with 16 heads per key head 40 us for 35, one of 32768 keys 26 for 22, the
+// error against 64 bits, 1.6e-3 of the output's own rounding, the same to two digits.)
 //
 // Keys and value columns are the rows of the products, 16 at a time, and the heads of a
 // group their 8 columns (two products for 9 to 16 heads): no row of a product is empty, and
@@ -54,7 +56,9 @@ using namespace ptx;
 
 constexpr int kOpen = 16;      // open rows of a unit
 constexpr int kJoinThreads = 256;
-constexpr float kGrow = 8.f;   // log2 units that a running maximum may lag behind: fp16 ends at 2^16
+constexpr float kGrow = 8.f;   // log2 units that a running maximum may lag behind
+constexpr float kTop = 12.f;   // log2 of a page's largest weight: fp16 ends at 2^16, four units are left for the
+                               // rounding of scores (of 2^24 and more) that it is taken from
 constexpr int kMaxCtas = 152;  // grid limit (sizes the workspace)
 constexpr int kMaxWarps = 8;   // of a CTA
 
@@ -341,7 +345,7 @@ struct State {
       }
     }
   }
-  // the unit's largest s + shift; what was summed so far goes along with the maximum
+  // x, a lane's largest scores, becomes the unit's; what was summed so far goes along with the maximum
   __device__ __forceinline__ void raise(float (&x)[NT][2]) {
     bool grow = false;
 #pragma unroll
@@ -485,8 +489,6 @@ __device__ __forceinline__ void page_unit(const Decode8Params& p, const Place& a
 #pragma unroll
     for (int t = 0; t < NT; ++t) f[t][0] = f[t][1] = 1.f;
   }
-  // the value scale's exponent: the products below stay under 2^(kGrow + 1)
-  const float shift = static_cast<float>((__float_as_int(scale.y) >> 23 & 255) - 127);
   float top[NT][2];
 #pragma unroll
   for (int t = 0; t < NT; ++t)
@@ -495,42 +497,59 @@ __device__ __forceinline__ void page_unit(const Decode8Params& p, const Place& a
       float most = s[t][0][e];
 #pragma unroll
       for (int j = 0; j < 4; ++j) most = max3(most, s[t][j][e], s[t][j][2 + e]);
-      top[t][e] = fmaf(most, f[t][e], shift);  // f is positive, or 0 where there is no head
+      top[t][e] = most * f[t][e];  // f is positive, or 0 where there is no head
     }
   x.raise(top);
-  // probabilities, rounded to fp16 and transposed: keys 2q, 2q + 1 of head r
+  // weights against the page's own maximum (a page whose keys are all masked: the running one), in fp16, transposed:
+  // keys 2q, 2q + 1 of head r.  g takes the page's sums of values to the running ones.
   uint32_t b[NT][4][2];
-  const uint64_t vs = both(scale.y);
+  uint64_t g[NT];
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
-    const uint64_t f2 = pack_f32x2(f[t][0], f[t][1]), base2 = pack_f32x2(-x.base(t, 0), -x.base(t, 1));
-    uint64_t sum2 = pack_f32x2(x.sum[t][0], x.sum[t][1]);
+    float of[2], to[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const float base = x.base(t, e), own = top[t][e] == -INFINITY ? base : top[t][e];
+      of[e] = kTop - own;
+      to[e] = ex2(-of[e] - base);  // what of rounds off, to puts back
+    }
+    const uint64_t f2 = pack_f32x2(f[t][0], f[t][1]), of2 = pack_f32x2(of[0], of[1]);
+    uint64_t sum2 = 0;
 #pragma unroll
     for (int j = 0; j < 4; ++j)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         float e0, e1;
-        unpack_f32x2(fma_f32x2(pack_f32x2(s[t][j][2 * e], s[t][j][2 * e + 1]), f2, base2), e0, e1);
-        const uint64_t ex = pack_f32x2(ex2(e0), ex2(e1));
-        sum2 = add_f32x2(sum2, ex);
-        unpack_f32x2(mul_f32x2(ex, vs), e0, e1);
+        unpack_f32x2(fma_f32x2(pack_f32x2(s[t][j][2 * e], s[t][j][2 * e + 1]), f2, of2), e0, e1);
+        e0 = ex2(e0);
+        e1 = ex2(e1);
+        sum2 = add_f32x2(sum2, pack_f32x2(e0, e1));
         b[t][j][e] = transposed(half_pair(e0, e1));
       }
-    unpack_f32x2(sum2, x.sum[t][0], x.sum[t][1]);
+    g[t] = pack_f32x2(to[0], to[1]);
+    unpack_f32x2(fma_f32x2(sum2, g[t], pack_f32x2(x.sum[t][0], x.sum[t][1])), x.sum[t][0], x.sum[t][1]);
+    g[t] = mul_f32x2(g[t], both(scale.y));
   }
 #pragma unroll
   for (int c = 0; c < DV / 16; ++c) {
     const uint4 v0 = *reinterpret_cast<const uint4*>(st + P::kVAt + (16 * c + r) * kPageRows + 16 * q);
     const uint4 v1 = *reinterpret_cast<const uint4*>(st + P::kVAt + (16 * c + 8 + r) * kPageRows + 16 * q);
     const uint32_t w0[4] = {v0.x, v0.y, v0.z, v0.w}, w1[4] = {v1.x, v1.y, v1.z, v1.w};
+    float o[NT][4] = {};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       uint32_t a[4];
       half_pairs(w0[j], a[0], a[2]);
       half_pairs(w1[j], a[1], a[3]);
 #pragma unroll
-      for (int t = 0; t < NT; ++t) product(x.o[t][c], a, b[t][j][0], b[t][j][1]);
+      for (int t = 0; t < NT; ++t) product(o[t], a, b[t][j][0], b[t][j][1]);
     }
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; e += 2)
+        unpack_f32x2(fma_f32x2(pack_f32x2(o[t][e], o[t][e + 1]), g[t], pack_f32x2(x.o[t][c][e], x.o[t][c][e + 1])),
+                     x.o[t][c][e], x.o[t][c][e + 1]);
   }
 }
 

@@ -508,3 +508,47 @@ def test_decode_small_scores_on_a_border(G):
     for window, sink in ((100, 0), (100, 7), (150, 70)):
         got = pkg.spa_attention_decode8(q, P, pages, table, blocks, kc, mul, vc, left, window=window, sink=sink)
         check_decode(got, *decode_reference(q, P, pages, table, blocks, kc, mul, vc, left, window, sink))
+
+
+@pytest.mark.parametrize("G", [1, 4, 12])
+@pytest.mark.parametrize("nats", [8, 12, 14, 16, 20])
+def test_decode_one_key_far_above(nats, G):
+    """A first key with most of the weight and a value of zero: the output is made of the small weights."""
+    pkg = spa()
+    g = gen(31 + nats + G)
+    d, m, dv, lens = 64, 32, 64, [8192, 8192 + 37]
+    pages, table, blocks, left = pool(g, pkg, lens, 1, m, dv)
+    kc, mul, vc = open_rows(g, 2, 1, 64, m, dv)
+    mul.mul_(2.0 ** -6)
+    P = (randn(g, 1, d, m) / math.sqrt(m)).to(BF16)
+    one = randn(g, d)
+    q = (one * torch.linspace(1.0, 0.9, G, device="cuda")[:, None]).expand(2, G, d).to(BF16).contiguous()
+    qp = one.double() @ P[0].double()
+    code = (qp * (300 / qp.abs().max())).to(F8)
+    for b in range(2):
+        for page in table[b, :blocks[b]].tolist():  # the others' logits: a deviation of a half
+            pages[1][page, 0] = 0.5 * math.sqrt(m) / (100 * float(qp.norm()))
+        first = int(table[b, 0])
+        bytes_of(pages[0])[first, 0] = 0
+        bytes_of(pages[0])[first, 0, 0] = bytes_of(code)
+        pages[1][first, 0] = nats * math.sqrt(m) / float(code.double() @ qp)
+        bytes_of(pages[2])[first, 0, :, PLACE[0]] = 0
+    got = pkg.spa_attention_decode8(q, P, pages, table, blocks, kc, mul, vc, left).double()
+    for b in range(2):
+        page = table[b, :blocks[b]].long()
+        r = int(left[b])
+        k = torch.cat((pages[0][page, 0].double().mul(pages[1][page, 0].double()[:, None, None]).flatten(0, 1),
+                       key_values(kc[b, 0, :r], mul[b, 0, :r])))
+        v = torch.cat((pages[2][page, 0].double()[:, :, PLACE].mul(pages[3][page, 0].double()[:, None, None])
+                       .transpose(1, 2).flatten(0, 1), vc[b, 0, :r].double()))
+        p = torch.softmax(q[b].double() @ P[0].double() @ k.T / math.sqrt(m), -1)
+        assert not v[0].any() and float(p[:, 0].min()) > 0.05
+        ref = p @ v
+        # As in decode_reference, but the first key's score and the sum of weights, of n additions one after the other
+        # at most, take all values by one factor.  A weight's own errors: its score, its rounding to fp16, and its
+        # place in a page's sum of 64 and a segment's of n / 64 pages.
+        size = (q[b].double().abs() @ P[0].double().abs() @ k.abs().T / math.sqrt(m)) * (
+            (d + m) * 2.0 ** -24 + 2.0 ** -21)
+        tol = (2 * size[:, :1] + len(k) * 2.0 ** -24) * ref.abs() + (
+            2 * size[:, 1:].amax(-1, keepdim=True) + 2.0 ** -11 + (len(k) / 64 + 64) * 2.0 ** -24) * (p @ v.abs())
+        check_decode(got[b], ref, tol)
