@@ -29,6 +29,8 @@ constexpr int kFwdBlocks = UPL > 1 ? 1 : INTER ? 4 : 3;  // blocks per SM that t
 template <int UPL, bool INTER>
 constexpr int kBwdBlocks = UPL > 1 ? 1 : 2;
 constexpr int kMaxVec = 16;  // features of a thread at most: UPL * (V, or 2 V of the two halves)
+// the gradient's vectors in the half layout: it holds twice the values (8: 142 us for 129 at the time, 4 x 8192 tokens)
+constexpr int kMaxHalfVec = 4;
 
 // V features of a row as they lie in memory, in whole registers: a load under a condition
 // then writes nothing but its registers and is waited for where the values are used.
@@ -611,11 +613,15 @@ cudaError_t launch(const NormRopeParams& p, cudaStream_t stream) {
     norm_rope_kernel<T, V, INTER, UPL, LOOSE, EXACT, E><<<all, kThreads, 0, stream>>>(p, it, lanes, units, turning);
     return cudaGetLastError();
   }
-  norm_rope_bwd_kernel<T, V, INTER, UPL, LOOSE, EXACT, EB><<<all, kThreads, 0, stream>>>(p, it, lanes, units, turning);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess || (!p.dw[0] && !p.dw[1])) return e;
-  const unsigned per_tensor = (p.d + kThreads / 32 - 1) / (kThreads / 32);
-  return ds::launch_after(norm_rope_sum_kernel, 2 * per_tensor, kThreads, 0, stream, p, it.first, all, per_tensor);
+  if constexpr (!INTER && V > kMaxHalfVec) {  // launch_norm_rope starts at vectors of kMaxHalfVec
+    return cudaErrorInvalidValue;
+  } else {
+    norm_rope_bwd_kernel<T, V, INTER, UPL, LOOSE, EXACT, EB><<<all, kThreads, 0, stream>>>(p, it, lanes, units, turning);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess || (!p.dw[0] && !p.dw[1])) return e;
+    const unsigned per_tensor = (p.d + kThreads / 32 - 1) / (kThreads / 32);
+    return ds::launch_after(norm_rope_sum_kernel, 2 * per_tensor, kThreads, 0, stream, p, it.first, all, per_tensor);
+  }
 }
 
 // d <= 256: with V features a vector a row has at most 256 / V units (INTER), or 128 / V.
@@ -647,9 +653,8 @@ cudaError_t launch_v(const NormRopeParams& p, int v, cudaStream_t stream) {
 
 cudaError_t launch_norm_rope(const NormRopeParams& p, cudaStream_t stream) {
   const int size = p.bf16 ? 2 : 4;
-  // the widest vector that every address allows: rows, halves and tail.  The gradient holds twice the values,
-  // 4 of each half at most (8: 142 us for 129 at the time, 4 x 8192 tokens)
-  int v = (p.g[0] || p.g[1]) && !p.interleaved ? 4 : 16 / size;
+  // the widest vector that every address allows: rows, halves and tail
+  int v = (p.g[0] || p.g[1]) && !p.interleaved ? kMaxHalfVec : 16 / size;
   auto fits = [&](int w) {
     const uintptr_t bytes = static_cast<uintptr_t>(w) * size;
     if (p.d % w) return false;

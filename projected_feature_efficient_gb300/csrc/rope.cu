@@ -28,6 +28,24 @@ namespace {
 
 constexpr int kThreads = 256;
 
+template <class T, int V>
+struct alignas(sizeof(T) * V) Vec {
+  T e[V];
+};
+
+// Two neighbouring elements of a vector at a time: one conversion of a bf16 pair.
+template <int V>
+__device__ __forceinline__ void put2(Vec<float, V>& w, int i, float x, float y) {
+  w.e[i] = x;
+  if (V > 1) w.e[V > 1 ? i + 1 : i] = y;
+}
+template <int V>
+__device__ __forceinline__ void put2(Vec<__nv_bfloat16, V>& w, int i, float x, float y) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(x, y);
+  w.e[i] = v.x;
+  if (V > 1) w.e[V > 1 ? i + 1 : i] = v.y;
+}
+
 // A thread's unit of a row: V elements (V/2 pairs) of an interleaved row, or V
 // elements of each half, or V elements of the tail.  LOOSE (interleaved, V = 2):
 // odd widths and strides, one feature at a time.

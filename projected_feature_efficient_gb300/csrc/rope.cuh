@@ -1,5 +1,5 @@
 // rope.cuh -- device helpers shared by the kernels that turn feature pairs by their
-// position (rope.cu, norm_rope.cu): vectors of a row, and sine and cosine of an angle
+// position (rope.cu, norm_rope.cu): a feature in fp32, and sine and cosine of an angle
 // that is held as a fraction of a turn.
 #pragma once
 #include <cstdint>
@@ -7,23 +7,6 @@
 
 namespace spa {
 
-template <class T, int V>
-struct alignas(sizeof(T) * V) Vec {
-  T e[V];
-};
-
-// Two neighbouring elements of a vector at a time: one conversion of a bf16 pair.
-template <int V>
-__device__ __forceinline__ void put2(Vec<float, V>& w, int i, float x, float y) {
-  w.e[i] = x;
-  if (V > 1) w.e[V > 1 ? i + 1 : i] = y;
-}
-template <int V>
-__device__ __forceinline__ void put2(Vec<__nv_bfloat16, V>& w, int i, float x, float y) {
-  const __nv_bfloat162 v = __floats2bfloat162_rn(x, y);
-  w.e[i] = v.x;
-  if (V > 1) w.e[V > 1 ? i + 1 : i] = v.y;
-}
 __device__ __forceinline__ float up(float x) { return x; }
 __device__ __forceinline__ float up(__nv_bfloat16 x) { return __bfloat162float(x); }
 
