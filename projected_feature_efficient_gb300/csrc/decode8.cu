@@ -7,7 +7,7 @@
 //   out = softmax(q~ K~^T / sqrt(m)) V,   q~ = q P_h,   K~ = ks * codes, V = vs * codes
 //
 //   decode8_query_kernel    q~ log2(e)/sqrt(m) of every row in two fp16 parts (22 bits)
-//   decode8_kernel          the keys: a warp takes a run of units (a page of 64 keys, or 32
+//   decode8_kernel          the keys: a warp takes a run of units (a page of 64 keys, or 16
 //                           open rows) of (sequence, key head, part of the group) in order
 //   decode8_combine_kernel  the parts of a row joined
 //
@@ -17,10 +17,11 @@
 // the largest, and rounded to fp16: 2^-12 of a weight for all down to 2^-(kTop + 14) of it,
 // 2^-(kTop + 25) of the largest below that.  The page's sums of weights and of weighted values
 // then join the running ones in fp32 by one factor.  (Against the running maximum, weights
-// 2^14 below it lost bits and 2^25 below it all, but not in the sum of weights: where a first
-// key of value zero lies 16 nats above 8192 others, a tenth of the output.  Two fp16 parts, 22
-// bits: 16 sequences with 16 heads per key head 40 us for 35, one of 32768 keys 26 for 22, the
-// error against 64 bits, 1.6e-3 of the output's own rounding, the same to two digits.)
+// 2^14 below it lost bits and 2^25 below it all, but not in the sum of weights: a first key of
+// value zero 20 nats above 8192 others left more than ten times the error that fp16 weights
+// account for.  Two fp16 parts, 22 bits: 16 sequences with 16 heads per key head 40 us for 35,
+// one of 32768 keys 26 for 22, the error against 64 bits, 1.6e-3 of the output's own rounding,
+// the same to two digits.)
 //
 // Keys and value columns are the rows of the products, 16 at a time, and the heads of a
 // group their 8 columns (two products for 9 to 16 heads): no row of a product is empty, and
@@ -212,7 +213,7 @@ struct Seq {
   int blocks, open;   // pages, open rows
   int lo;             // first key of the window
   int sb, wb;         // pages [0, sb) hold first keys that stay visible, [wb, blocks) the window
-  int units;          // pages, then open rows, 32 to a unit
+  int units;          // pages, then open rows, 16 to a unit
 };
 __device__ __forceinline__ Seq seq_of(const Decode8Params& p, int b) {
   Seq s;
