@@ -36,13 +36,13 @@
 // operands of four value products with one 16-byte load.
 //
 // 64 sequences of up to 8191 keys, 32 heads on 8 key heads, m = 32, d_v = 128 (340 MB,
-// 51 us at the rate of a copy): 67 us for the call, 5.1 TB/s; without the products 65 us, so
+// 51 us at the rate of a copy): 68 us for the call, 5.0 TB/s; without the products 65 us, so
 // they hide behind the copies.  The first page is there after 8 us (queries, lengths, table
 // and page follow on one another), the middle warp ends at 53 us and the last at 62, because
 // memory does not serve all SMs alike.  Giving out three sixteenths of each segment's units
 // late, in chunks to warps that are done, brought the ends together but cost as much in
 // chunks' first loads and sums (74 us).  Looking for a row's parts before the wait for the
-// keys' kernel instead of after it: 72 -> 67 us.
+// keys' kernel instead of after it: 72 -> 67 us at the time.
 #include <cuda_fp16.h>
 #include <math.h>
 

@@ -12,8 +12,8 @@
 // A group of neighbouring lanes holds a row, a lane the same features of every row that it
 // sees, so that sines, weights and the sums of dw stay in its registers, and a row's sums
 // take a few shuffles.  2 x 8192 tokens of 20 heads, d = 128, bf16: 168 MB, 31 us (5.4 TB/s,
-// 25 us at the rate of a copy); the gradient of 4 x 8192: 503 MB, 106 us and 8 for the sums of
-// dw (4.8 TB/s; 75 us).  What is left is the instructions: they issue in 59% and 54% of the
+// 25 us at the rate of a copy); the gradient of 4 x 8192: 503 MB, 106 us and 7 for the sums of
+// dw (4.8 TB/s; 75 us); 8191 tokens of 16 heads of 96 in fp32: 101 MB, 25 us a call (15 us).  What is left is the instructions: they issue in 59% and 54% of the
 // cycles, and 107 registers of the gradient leave room for two blocks per SM.
 #include "decode_shared.cuh"
 #include "kernels.cuh"

@@ -192,12 +192,11 @@ __global__ void __launch_bounds__(128) project_kernel(const ProjParams p) {
   __shared__ float red[4];
   const int tile = blockIdx.x, bh = blockIdx.y, which = blockIdx.z;
   const int tid = threadIdx.x;
-  if (which && p.group > 1 && bh >= p.BH / p.group) return;
   const int d = p.d, m = p.m;
   float* Ps = psm;              // [d][MP]
   float* xs = psm + d * MP;     // [128][33]
 
-  const T* P = static_cast<const T*>(p.P) + static_cast<size_t>(proj_head(p, which, bh)) * d * m;
+  const T* P = static_cast<const T*>(p.P) + static_cast<size_t>(bh % p.H) * d * m;
   for (int i = tid; i < d * MP; i += 128) {
     const int l = i / MP, k = i % MP;
     Ps[i] = k < m ? to_f(P[l * m + k]) : 0.f;
