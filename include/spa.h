@@ -518,7 +518,8 @@ SPA_API int spa_attention_window_bwd(const void *q, const void *k, const void *v
  *     be its input (same strides); any other overlap is not allowed.
  *   1 <= d <= 256, rot even, 0 <= rot <= d, eps > 0 and finite, at most 2^31 rows
  *   in a tensor (else SPA_ERR_SHAPE).  Arithmetic is fp32, one rounding at the
- *   end; the squares of a row must not overflow fp32.
+ *   end; the squares of a row must not overflow fp32.  A row with a value that is
+ *   not finite shows it in its own outputs (and dw) alone.
  * spa_norm_rope_bwd -- the gradient: from the inputs q, k again and the outputs'
  *   gradients dq_out, dk_out, with u = R^T dy, t = w * u,
  *     dx = r t - x r^3 (sum_i t_i x_i) / d,    dw = sum over rows of u * x r.
